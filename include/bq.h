@@ -30,6 +30,12 @@
  *   bq_linear_group                     up to 4 layers sharing their input x, one launch
  *   bq_linear_static_scratch            bq_linear with a fixed library scratch array
  *   bq_linear_plan                      the work split of bq_linear / bq_gemm (host only)
+ * and, beside the packed formats, plain symmetric 8-bit layers on row-major int8 codes with a
+ * scale per token and a scale per output channel, for any number of tokens (below, "Scaled int8"):
+ *   bq_scaled_quantize                  per-row int8 codes and scales (tokens or weight rows)
+ *   bq_scaled_gemm                      int8 x int8 product, both scales and the bias applied
+ *   bq_scaled_gemm_grouped              the same, rows grouped by expert with ragged sizes
+ *   bq_scaled_linear                    quantization of x and the product in one call
  * Pack options (bq_pack_desc): RaBiT iterative residual SVID initialisation of g and h
  * (rabit_svid_rounds, "RaBiT框架" page §2.3); ABQ bit-balance W2* (abq_bit_balance,
  * "ABQ-LLM" page §3.3); ABQ distribution compensation W + a b^T (abq_comp_a, abq_comp_b,
@@ -343,6 +349,70 @@ typedef struct {
   uint32_t shared_bytes;          /* dynamic shared memory per CTA */
 } bq_plan_info;
 bq_status bq_linear_plan(const bq_layer* layer, int32_t M, int32_t fused, bq_plan_info* info);
+
+/* ------------------------------------------------------------------------------------
+ * Scaled int8: layers whose weights are plain int8 codes with one scale per output channel,
+ * W_hat[n][k] = scale[n] codes[n][k], on activations quantized to int8 with one scale per token.
+ * No packed buffer and no act buffer: codes are row-major matrices the caller may have loaded
+ * from a checkpoint, scales are f32 vectors.
+ *
+ * Layout rules. Every matrix of codes starts on a 16-byte boundary and so does every row of it:
+ * ld (bytes between rows) is a multiple of 16, >= K and < 2^36. K itself is free (1..BQ_MAX_K); bytes
+ * K..ld-1 of a row are neither read nor written. x, gate and y are matrices of `bq_type` with
+ * any row stride >= the row (in elements), aligned to their element. Outputs must not overlap
+ * inputs. Limits: 1 <= N <= BQ_MAX_N, 1 <= K <= BQ_MAX_K, 0 <= M < 2^31 - 2^16 (M = 0 is a no-op),
+ * 1 <= experts <= BQ_MAX_EXPERTS.
+ * ------------------------------------------------------------------------------------ */
+typedef enum { BQ_TYPE_F32 = 0, BQ_TYPE_BF16 = 1, BQ_TYPE_F16 = 2 } bq_type; /* f32, bf16, f16 */
+#define BQ_MAX_EXPERTS 1024
+
+/* The weights of one layer (experts = 1) or of one layer per expert. Device pointers. */
+typedef struct {
+  const int8_t* codes;    /* [experts][N][K], rows ld bytes apart, experts expert_stride bytes apart */
+  const float* scale;     /* [experts][N] */
+  const float* bias;      /* [experts][N], or NULL */
+  int64_t ld;
+  int64_t expert_stride;  /* a multiple of 16, >= 0 and < 2^39; ignored when experts = 1 */
+  int32_t N, K, experts;
+} bq_scaled_weights;
+
+/* q[i][k] and scale[i] (i < M) from row r of x [x_rows][K], r = i, or rows[i] where `rows`
+ * (nullable, device int32 [M]) is given: the gather of tokens into the experts' order.
+ *   v[k] = x[r][k], or x[r][k] * (g / (1 + exp(-g))) with g = gate[r][k] where `gate` (nullable,
+ *   same type and shape as x, its own row stride ldg) is given, in f32;
+ *   gamma = max_k |v[k]|;  s = 127 * (1 / gamma);  q = rn(v * s), the reciprocal and both products
+ *   rounded to f32, ties to even;  scale = gamma / 127.
+ * Rows with gamma < 2^-100 get q = 0 and scale = 0. A row that holds a NaN or an infinity (or
+ * whose gated value does) gets q = 0 and scale = NaN, so every output made from it is NaN and no
+ * other row is touched. rows[i] < 0 is an empty slot: q = 0, scale = 0. rows[i] >= x_rows: q = 0,
+ * scale = NaN and the device error word is raised (bq_device_check). The same call quantizes
+ * weights: one row per output channel. Without `rows`, x_rows >= M. */
+bq_status bq_scaled_quantize(const void* x, int32_t x_type, int64_t ldx, int32_t x_rows, const void* gate,
+                             int64_t ldg, const int32_t* rows, int32_t M, int32_t K, int8_t* q, int64_t ldq,
+                             float* scale, void* stream);
+
+/* y[m][n] = (float)(sum_k q[m][k] codes[n][k]) * (scale[m] * w.scale[n]) + w.bias[n], one expert.
+ * The sum is exact (int32; codes may be -128). The sum, the product of the scales, their product
+ * and the sum with the bias are each rounded to f32 (a bias is added by one fused multiply-add),
+ * then y is rounded once to y_type. */
+bq_status bq_scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_t ldq, const float* scale, int32_t M,
+                         void* y, int32_t y_type, int64_t ldy, void* stream);
+
+/* bq_scaled_gemm with expert e's weights for the rows offsets[e] <= m < offsets[e+1]; `offsets`
+ * (device int32 [experts + 1]) is read by the kernel, so no host synchronization is needed and a
+ * captured graph follows its contents. 0 <= offsets[0] <= offsets[1] <= ... <= M; experts may be
+ * empty. Rows before offsets[0] and from offsets[experts] on keep what y held. Offsets that
+ * decrease or leave [0, M]: y is left as it was and the device error word is raised. */
+bq_status bq_scaled_gemm_grouped(const bq_scaled_weights* w, const int8_t* q, int64_t ldq, const float* scale,
+                                 int32_t M, const int32_t* offsets, void* y, int32_t y_type, int64_t ldy,
+                                 void* stream);
+
+/* bq_scaled_quantize of x [M][K] into `workspace` (device, 256-byte aligned, at least
+ * bq_scaled_workspace_bytes), then bq_scaled_gemm from it: same results as the two calls. */
+bq_status bq_scaled_workspace_bytes(const bq_scaled_weights* w, int32_t M, size_t* bytes);
+bq_status bq_scaled_linear(const bq_scaled_weights* w, const void* x, int32_t x_type, int64_t ldx, int32_t M,
+                           void* y, int32_t y_type, int64_t ldy, void* workspace, size_t workspace_bytes,
+                           void* stream);
 
 /* Synchronizes the current device, then reads and clears the device error word:
  * BQ_OK or BQ_ERR_DEVICE_CHECK. */
