@@ -410,13 +410,12 @@ inline cudaError_t launch_fmt(const PkLayout& L, const LayerArgs& g, int NW, dim
 // ABQ with 16..64 tokens (from an act buffer) runs on the tensor cores.
 inline bool tc_eligible(const PkLayout& L, int M) { return tc_layer(L.fmt, L.w_bits, M); }
 
-// The packed weight tiles of a layer as the tensor-core kernel's 3-D TMA map (TcTensorMap).
 // cuTensorMapEncodeTiled is a host-side encode (no device work), resolved once through the
-// runtime like the context query above.
-inline bool encode_weight_map(const PkLayout& L, const void* tiles, TcTensorMap* out) {
-  typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// runtime like the context query above. Null without a driver.
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline EncodeTiled encode_tiled() {
   static_assert(sizeof(TcTensorMap) == sizeof(CUtensorMap), "tensor map size");
   static EncodeTiled encode = nullptr;
   static std::once_flag once;
@@ -428,6 +427,12 @@ inline bool encode_weight_map(const PkLayout& L, const void* tiles, TcTensorMap*
       encode = reinterpret_cast<EncodeTiled>(f);
     (void)cudaGetLastError();
   });
+  return encode;
+}
+
+// The packed weight tiles of a layer as the tensor-core kernel's 3-D TMA map (TcTensorMap).
+inline bool encode_weight_map(const PkLayout& L, const void* tiles, TcTensorMap* out) {
+  const EncodeTiled encode = encode_tiled();
   if (!encode) return false;
   const cuuint64_t dims[3] = {256u, cuuint64_t(L.KT) * L.tile_bytes / 256u, cuuint64_t(L.RB)};
   const cuuint64_t strides[2] = {256u, cuuint64_t(L.KT) * L.tile_bytes};  // bytes, dims 1 and 2

@@ -4,7 +4,7 @@
 
 #include <cuda_fp16.h>
 
-#include "bq_gemv.cuh"
+#include "bq_tc.cuh"
 
 namespace bqi {
 
@@ -112,82 +112,379 @@ __global__ void __launch_bounds__(256) k_scaled_quantize(const SqArgs a) {
 // ---------------------------------------------------------------------------
 // product
 // ---------------------------------------------------------------------------
+//
+// y^T = W q^T on the fifth-generation tensor cores: tcgen05.mma kind::i8 (s8 x s8 -> s32), the
+// weights as the MMA's M (128 channels a CTA) and the tokens as its N. Channels are many and
+// their number is known, tokens are few, ragged or both: a tile of n tokens costs an MMA of N = n
+// rounded up to 16 (32 for a CTA pair), not a whole 128 or 256 rows.
+//
+// Both operands are K-major rows of codes, copied by TMA in boxes of 128 bytes of k by 128
+// channels or n tokens with the 128-byte swizzle, which is the layout the MMA reads. Rows past the
+// matrices and k past K read as zero, so K and N need no padding in memory. CG = 2: the two CTAs of
+// a cluster hold 128 channels and half of the tokens each, and one MMA of M = 256 reads both.
+//
+// Warp roles, coupled only by mbarriers: warps 0-3 are the epilogue (tensor-memory lanes 32w ..),
+// warp 4 copies, warp 5 issues the MMAs. Accumulators are double-buffered in tensor memory, so the
+// copies and MMAs of the next tile run under this tile's epilogue; the kernel is persistent, tile t
+// of the CTA (pair) c is c, c + grid, ...
+//
+// Every wait is bounded and ends when another role has stopped; then the error word is raised,
+// the peer is told, copies in flight are waited for and the tensor memory is freed.
+
+constexpr int kSgRows = 128;       // channels per CTA
+constexpr int kSgChunk = 128;      // bytes of k per stage
+constexpr int kSgThreads = 192;
+constexpr int kSgCopyWarp = 4, kSgMmaWarp = 5;
+constexpr int kSgMaxStages = 12;
+constexpr int kSgMaxTokens = 256;  // tokens per tile at most
+constexpr uint32_t kSgWBytes = kSgRows * kSgChunk;
+// shared memory: alignment slack, the stages (each a multiple of 1024 bytes), then this region:
+// full[12] (0), empty[12] (96), acc_full[2] (192), acc_empty[2] (208), words[8] (224), token scales
+// [2][256] (256); then, grouped, the first tile of every expert [E + 1]
+constexpr uint32_t kSgRegion = 256 + 2 * kSgMaxTokens * 4;
 
 struct SgArgs {
-  const int8_t* w;
+  TcTensorMap wmap, qmap, qmap16;  // weights; tokens in boxes of a whole tile, and of 16 rows
   const float* w_scale;
-  const float* bias;    // or null
-  const int8_t* q;
+  const float* bias;               // or null
   const float* scale;
-  const int* offsets;   // or null: one group of M rows
+  const int* offsets;              // or null: one group of M rows
   void* y;
-  long long ldw, expert_stride, ldq, ldy;
+  long long ldy;
   int M, N, K, E, y_type;
+  int w_experts;                   // distinct weight matrices: E, or 1 where the experts share one
+  int bn;                          // tokens per tile at most, a multiple of 16 CG
+  int stages, stage_bytes, cols, acc_stride;  // tensor-memory columns, and between accumulators
+  int splits;                      // CTAs that share a tile's k-range (split kernel)
 };
 
-__device__ __forceinline__ void sg_store(const SgArgs& a, long long at, float v) {
-  if (a.y_type == BQ_TYPE_F32) static_cast<float*>(a.y)[at] = v;
-  else if (a.y_type == BQ_TYPE_BF16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
-  else static_cast<__half*>(a.y)[at] = __float2half_rn(v);
+// Shared-memory descriptor of a K-major operand in 128-byte swizzled rows: start address, 1024
+// bytes between 8-row groups, version 1, layout type 2 (the leading offset is not used).
+__device__ __forceinline__ uint64_t sg_desc(uint32_t saddr) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t(64) << 32) | (uint64_t(1) << 46) |
+         (uint64_t(2) << 61);
+}
+// kind::i8 with s32 accumulators, s8 x s8, both K-major
+__device__ __forceinline__ uint32_t sg_idesc(int n, int m) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+template <int CG>
+__device__ __forceinline__ void sg_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accum) {
+  if constexpr (CG == 1)
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(int(accum))
+                 : "memory");
+  else
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(int(accum))
+                 : "memory");
+}
+// completion of this thread's MMAs so far, on bar of this CTA (CG = 1) or of both CTAs of the pair
+template <int CG>
+__device__ __forceinline__ void sg_commit(uint64_t* bar, uint32_t pair_mask) {
+  if constexpr (CG == 1)
+    tc_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+            smem_u32(bar)),
+        "h"(uint16_t(pair_mask))
+        : "memory");
+}
+// one box into this CTA's shared memory, completing on the barrier at (cluster) address bar
+template <int CG>
+__device__ __forceinline__ void sg_copy_2d(void* dst, const TcTensorMap* map, int x, int y, uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void sg_copy_3d(void* dst, const TcTensorMap* map, int x, int y, int z, uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void sg_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
 
-// 64 rows x 64 channels a block, K in pieces of 64 bytes through shared memory, four by four
-// outputs a thread with 4-byte dot products. Block y is the y-th 64-row tile, counted group by group.
-__global__ void __launch_bounds__(256) k_scaled_gemm(const SgArgs a) {
-  __shared__ int As[16][65], Bs[16][65];
-  int e = 0, m0 = blockIdx.y * 64, hi = a.M;
-  if (a.offsets) {
-    bool ok = a.offsets[0] >= 0 && a.offsets[a.E] <= a.M;
-    int tile = blockIdx.y;
-    bool found = false;
-    for (int i = 0; i < a.E; i++) {
-      const int lo = a.offsets[i], up = a.offsets[i + 1];
-      if (up < lo) ok = false;
-      const int n = (up - lo + 63) / 64;
-      if (!found) {
-        if (tile < n) { e = i; m0 = lo + 64 * tile; hi = up; found = true; }
-        else tile -= n;
-      }
-    }
-    if (!ok) {
-      if (threadIdx.x == 0) atomicOr(&g_bq_device_error, kErrScaledIndex);
-      return;
-    }
-    if (!found) return;
+__device__ __forceinline__ float sg_value(uint32_t acc, float s, float b, bool bias) {
+  const float v = float(int(acc));
+  return bias ? __fmaf_rn(v, s, b) : __fmul_rn(v, s);
+}
+__device__ __forceinline__ void sg_put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void sg_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void sg_put(__half* p, float v) { *p = __float2half_rn(v); }
+
+// One tile of work: tokens m0 .. m0 + n - 1 of expert e against the channels from n0 on.
+struct SgTile {
+  int e, m0, n, n0;
+};
+
+// Walks a CTA's (or pair's) tiles in order. Tiles are numbered expert by expert, and within one in
+// bands of 8 token tiles that run along the channels, so that tiles in flight at the same time share
+// rows of both operands in the L2.
+struct SgWalk {
+  const SgArgs& a;
+  const int* first;  // grouped: first tile of every expert (shared memory)
+  int step, total, nt, e;
+  __device__ __forceinline__ SgWalk(const SgArgs& args, const int* first_tile, int channels)
+      : a(args), first(first_tile), step(channels), nt((args.N + channels - 1) / channels), e(0) {
+    total = a.offsets ? first[a.E] : (a.M + a.bn - 1) / a.bn * nt;
   }
-  const int n0 = blockIdx.x * 64, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int8_t* w = a.w + e * a.expert_stride;
-  int acc[4][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += 64) {
-    for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-      const int row = i >> 4, c = i & 15, k = k0 + 4 * c;
-      uint32_t va = 0, vb = 0;
-      for (int b = 0; b < 4 && k + b < a.K; b++) {
-        if (m0 + row < hi) va |= uint32_t(uint8_t(a.q[(long long)(m0 + row) * a.ldq + k + b])) << (8 * b);
-        if (n0 + row < a.N) vb |= uint32_t(uint8_t(w[(long long)(n0 + row) * a.ldw + k + b])) << (8 * b);
-      }
-      As[c][row] = int(va);
-      Bs[c][row] = int(vb);
+  __device__ __forceinline__ bool at(int t, SgTile* o) {
+    if (t >= total) return false;
+    int lo = 0, hi = a.M, r = t;
+    if (a.offsets) {
+      while (first[e + 1] <= t) e++;
+      lo = __ldg(a.offsets + e);
+      hi = __ldg(a.offsets + e + 1);
+      r = t - first[e];
     }
-    __syncthreads();
-#pragma unroll 4
-    for (int c = 0; c < 16; c++)
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-#pragma unroll
-        for (int j = 0; j < 4; j++) acc[i][j] = __dp4a(As[c][ty + 16 * i], Bs[c][tx + 16 * j], acc[i][j]);
-    __syncthreads();
+    const int mt = (hi - lo + a.bn - 1) / a.bn;
+    const int band = r / (8 * nt), m_first = 8 * band, gm = min(8, mt - m_first);
+    r -= band * 8 * nt;
+    const int m = m_first + r % gm;
+    o->e = e;
+    o->n0 = r / gm * step;
+    o->m0 = lo + m * a.bn;
+    o->n = min(a.bn, hi - o->m0);
+    return true;
   }
-  for (int i = 0; i < 4; i++)
-    for (int j = 0; j < 4; j++) {
-      const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m < hi && n < a.N) {
-        const long long wn = (long long)e * a.N + n;
-        const float s = __fmul_rn(a.scale[m], a.w_scale[wn]);
-        const float v = float(acc[i][j]);
-        sg_store(a, m * a.ldy + n, a.bias ? __fmaf_rn(v, s, a.bias[wn]) : __fmul_rn(v, s));
+};
+
+// First tile of every expert from the offsets (warp 0): first[E] is their number, or 0 and *bad = 1
+// where the offsets decrease or leave [0, M].
+__device__ __forceinline__ void sg_first_tiles(const SgArgs& a, int* first, int channels, uint32_t* bad, int lane) {
+  const int nt = (a.N + channels - 1) / channels;
+  int base = 0;
+  bool wrong = false;
+  for (int i0 = 0; i0 < a.E; i0 += 32) {
+    const int i = i0 + lane;
+    int tiles = 0;
+    if (i < a.E) {
+      const int lo = __ldg(a.offsets + i), hi = __ldg(a.offsets + i + 1);
+      if (lo < 0 || hi < lo || hi > a.M) wrong = true;
+      else tiles = (hi - lo + a.bn - 1) / a.bn * nt;
+    }
+    int sum = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (i < a.E) first[i] = base + sum - tiles;
+    base += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  wrong = __any_sync(0xffffffffu, wrong);
+  if (lane == 0) {
+    first[a.E] = wrong ? 0 : base;
+    *bad = wrong;
+  }
+}
+
+// This warp's 32 channels of a tile: tensor-memory lanes to y, column by column (a token's 32
+// channels are one 64- or 128-byte store).
+template <typename Y>
+__device__ __forceinline__ void sg_epilogue(const SgArgs& a, const SgTile& t, uint32_t acc, const float* tok, int n,
+                                            float sw, float b) {
+  Y* y = static_cast<Y*>(a.y) + (long long)t.m0 * a.ldy + n;
+  const bool bias = a.bias != nullptr, live = n < a.N;
+  for (int c = 0; c < t.n; c += 32) {
+    uint32_t v[32];
+    tc_ld32(acc + uint32_t(c), v);
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < 32; i++)
+        if (c + i < t.n) sg_put(y + (long long)(c + i) * a.ldy, sg_value(v[i], __fmul_rn(tok[c + i], sw), b, bias));
+    }
+  }
+}
+
+template <int CG>
+__global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_constant__ SgArgs a) {
+  extern __shared__ __align__(128) uint8_t sg_smem[];
+  const uint32_t pad = (1024u - (smem_u32(sg_smem) & 1023u)) & 1023u;
+  uint8_t* stages = sg_smem + pad;
+  uint8_t* region = stages + size_t(a.stages) * a.stage_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(region);
+  uint64_t* empty = full + kSgMaxStages;
+  uint64_t* acc_full = empty + kSgMaxStages;
+  uint64_t* acc_empty = acc_full + 2;
+  // words: [0] tensor-memory address, [1] a role stopped, [2] bad offsets, [3] copies issued
+  uint32_t* words = reinterpret_cast<uint32_t*>(region + 224);
+  float* tok = reinterpret_cast<float*>(region + 256);
+  int* first = reinterpret_cast<int*>(region + kSgRegion);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = a.stages;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  const int kc = (a.K + kSgChunk - 1) / kSgChunk;
+  const int unit = blockIdx.x / CG, units = gridDim.x / CG;
+  uint32_t* stop = &words[1];
+
+  if (tid == 0) {
+    for (int i = 0; i < S; i++) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4 * CG);
+    }
+    fence_mbar_init();
+    for (int i = 1; i < 8; i++) words[i] = 0;
+  }
+  if (warp == kSgMmaWarp) {
+    if constexpr (CG == 1) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(words)), "r"(a.cols) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(words)), "r"(a.cols) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+    }
+  }
+  pdl_wait();
+  __syncthreads();  // words[2] is zeroed before the scan may set it
+  if (warp == 0 && a.offsets) sg_first_tiles(a, first, kSgRows * CG, &words[2], lane);
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();  // the peer's barriers and tensor memory are ready
+  tc_fence_after();
+  const uint32_t tmem = words[0];
+  SgWalk walk(a, first, kSgRows * CG);
+  SgTile t;
+  // this CTA's failure is told to its peer, whose waits then end too
+  auto give_up = [&]() {
+    *reinterpret_cast<volatile uint32_t*>(stop) = 1u;
+    if constexpr (CG == 2)
+      asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(dsmem_map(smem_u32(stop), rank ^ 1u)), "r"(1u) : "memory");
+  };
+
+  if (warp == kSgCopyWarp) {
+    if (lane == 0) {
+      int st = 0, issued = 0;
+      uint32_t ph = 1;
+      bool ok = true;
+      for (int u = unit; ok && walk.at(u, &t); u += units) {
+        const int nn = (t.n + 16 * CG - 1) / (16 * CG) * (16 * CG), part = nn / CG;  // tokens of the MMA, and of this CTA
+        const uint32_t bytes = CG * (kSgWBytes + uint32_t(part) * kSgChunk);
+        for (int k = 0; k < kc; k++) {
+          if (!(ok = tc_wait(&empty[st], ph, stop))) break;
+          uint8_t* dst = stages + size_t(st) * a.stage_bytes;
+          const uint32_t bar = CG == 2 ? dsmem_map(smem_u32(&full[st]), 0u) : smem_u32(&full[st]);
+          if (rank == 0) mbar_expect_tx(&full[st], bytes);
+          sg_copy_3d<CG>(dst, &a.wmap, k * kSgChunk, t.n0 + int(rank) * kSgRows, min(t.e, a.w_experts - 1), bar);
+          const int m = t.m0 + int(rank) * part;
+          if (part * CG == a.bn) {
+            sg_copy_2d<CG>(dst + kSgWBytes, &a.qmap, k * kSgChunk, m, bar);
+          } else {
+            for (int i = 0; i < part; i += 16)
+              sg_copy_2d<CG>(dst + kSgWBytes + i * kSgChunk, &a.qmap16, k * kSgChunk, m + i, bar);
+          }
+          issued++;
+          if (++st == S) { st = 0; ph ^= 1; }
+        }
+      }
+      if (!ok) give_up();
+      words[3] = uint32_t(issued);
+      // every stage's last MMAs have read it (and their arrivals have landed) before this CTA may end
+      for (int i = 0; i < min(S, issued) && ok; i++) {
+        if (--st < 0) { st = S - 1; ph ^= 1; }
+        ok = tc_wait(&empty[st], ph ^ 1u, stop);
       }
     }
+  } else if (warp == kSgMmaWarp) {
+    if (lane == 0 && rank == 0) {
+      int st = 0, i = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int u = unit; ok && walk.at(u, &t); u += units, i++) {
+        const int nn = (t.n + 16 * CG - 1) / (16 * CG) * (16 * CG), buf = i & 1;
+        const uint32_t idesc = sg_idesc(nn, kSgRows * CG), d = tmem + uint32_t(buf * a.acc_stride);
+        if (!(ok = tc_wait(&acc_empty[buf], uint32_t((i >> 1) & 1) ^ 1u, stop))) break;
+        tc_fence_after();
+        for (int k = 0; k < kc; k++) {
+          if (!(ok = tc_wait(&full[st], ph, stop))) break;
+          tc_fence_after();
+          const uint32_t wa = smem_u32(stages + size_t(st) * a.stage_bytes);
+          const uint64_t da = sg_desc(wa), db = sg_desc(wa + kSgWBytes);
+          const int pieces = min(4, (a.K - k * kSgChunk + 31) / 32);
+          for (int j = 0; j < pieces; j++) sg_mma<CG>(d, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
+          sg_commit<CG>(&empty[st], 3u);
+          if (++st == S) { st = 0; ph ^= 1; }
+        }
+        if (ok) sg_commit<CG>(&acc_full[buf], 3u);
+      }
+      if (!ok) give_up();
+    }
+  } else {
+    bool ok = true;
+    const uint32_t lanes = uint32_t(32 * warp) << 16;
+    int i = 0;
+    for (int u = unit; walk.at(u, &t); u += units, i++) {
+      const int buf = i & 1;
+      float* tk = tok + buf * kSgMaxTokens;
+      for (int j = tid; j < t.n; j += 128) tk[j] = __ldg(a.scale + t.m0 + j);
+      const int n = t.n0 + int(rank) * kSgRows + tid;
+      const long long wn = (long long)t.e * a.N + n;
+      const float sw = n < a.N ? __ldg(a.w_scale + wn) : 0.f, b = a.bias && n < a.N ? __ldg(a.bias + wn) : 0.f;
+      asm volatile("bar.sync 1, 128;\n" ::: "memory");  // the scales are written (buffer i - 2 was read before tile i - 1's)
+      ok = __all_sync(0xffffffffu, tc_wait(&acc_full[buf], uint32_t((i >> 1) & 1), stop));
+      if (ok) {
+        tc_fence_after();
+        const uint32_t acc = tmem + lanes + uint32_t(buf * a.acc_stride);
+        if (a.y_type == BQ_TYPE_F32) sg_epilogue<float>(a, t, acc, tk, n, sw, b);
+        else if (a.y_type == BQ_TYPE_BF16) sg_epilogue<__nv_bfloat16>(a, t, acc, tk, n, sw, b);
+        else sg_epilogue<__half>(a, t, acc, tk, n, sw, b);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2) sg_arrive_at(dsmem_map(smem_u32(&acc_empty[buf]), 0u));
+          else mbar_arrive(&acc_empty[buf]);
+        }
+      } else if (lane == 0) {
+        give_up();
+      }
+      // a warp that gave up still takes the tiles' barriers with the others, without waiting for MMAs
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    if (words[2]) atomicOr(&g_bq_device_error, kErrScaledIndex);
+    if (words[1]) {  // a role gave up: copies it had issued are given time to land
+      const int issued = int(words[3]);
+      if (rank == 0)
+        for (int j = max(0, issued - S); j < issued; j++) mbar_wait_bounded(&full[j % S], uint32_t((j / S) & 1));
+      for (int j = 0; j < 1000; j++) __nanosleep(1000);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();  // no arrival of the peer is still on its way
+  if (warp == kSgMmaWarp) {
+    tc_fence_after();
+    if constexpr (CG == 1)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(a.cols) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(a.cols) : "memory");
+  }
 }
 
 }  // namespace bqi

@@ -50,12 +50,81 @@ inline cudaError_t launch_scaled_quantize(const SqArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-inline bq_status launch_scaled_gemm(const SgArgs& a, cudaStream_t s) {
-  const long long tiles = (long long)(a.M + 63) / 64 + (a.offsets ? a.E : 0);
-  const dim3 grid(unsigned((a.N + 63) / 64), unsigned(std::min(tiles, 65535ll)));
-  if (tiles > 65535) return BQ_ERR_UNSUPPORTED;
-  k_scaled_gemm<<<grid, 256, 0, s>>>(a);
-  return launch_status();
+// Rows of int8 codes as a TMA map with 128-byte swizzle: [experts][rows][K], boxes of 128 bytes by
+// box_rows. Rows and k past the matrix read as zero.
+inline bool encode_codes_map(const int8_t* p, int64_t ld, int64_t rows, int K, int E, int64_t expert_stride,
+                             int box_rows, TcTensorMap* out) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(K), cuuint64_t(rows), cuuint64_t(E)};
+  const cuuint64_t strides[2] = {cuuint64_t(ld), cuuint64_t(E > 1 ? expert_stride : 16)};
+  const cuuint32_t box[3] = {cuuint32_t(kSgChunk), cuuint32_t(box_rows), 1u};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUtensorMap m;
+  if (encode(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, E > 0 ? 3 : 2, const_cast<int8_t*>(p), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  std::memcpy(out, &m, sizeof(m));
+  return true;
+}
+
+struct SgPlan {
+  int cg, bn, stages;
+  uint32_t smem;
+};
+
+inline SgPlan plan_scaled_gemm(int M, int E, bool grouped) {
+  SgPlan p{};
+  const long long rows = grouped ? ((long long)M + E - 1) / E : M;  // of one expert, on average
+  const long long most = grouped ? std::min<long long>(M, 2 * rows) : M;
+  if (rows <= 64) {
+    p.cg = 1;
+    p.bn = int(std::min<long long>(64, (most + 15) / 16 * 16));
+  } else {
+    p.cg = 2;
+    p.bn = int(std::min<long long>(256, (most + 31) / 32 * 32));
+  }
+  const uint32_t stage = kSgWBytes + uint32_t(p.bn / p.cg) * kSgChunk;
+  const uint32_t fixed = 1024 + kSgRegion + (grouped ? 4u * uint32_t(E + 1) : 0u);
+  p.stages = std::min(kSgMaxStages, int((kTcSmemMax - fixed) / stage));
+  p.smem = fixed + uint32_t(p.stages) * stage;
+  return p;
+}
+
+template <int CG>
+inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long tiles, cudaStream_t s) {
+  auto k = k_scaled_tc<CG>;
+  static std::mutex mu;
+  static unsigned long long set_ctx = 0;
+  {
+    const unsigned long long ctx = current_context_id();
+    std::lock_guard<std::mutex> lock(mu);
+    if (ctx == 0 || ctx != set_ctx) {
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kTcSmemMax)) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return BQ_ERR_CUDA;
+      }
+      set_ctx = ctx;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(CG * std::min<long long>(tiles, sm_count() / CG)));
+  cfg.blockDim = dim3(kSgThreads);
+  cfg.dynamicSmemBytes = p.smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(CG);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = CG > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, k, a) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return BQ_ERR_CUDA;
+  }
+  return BQ_OK;
 }
 
 inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_t ldq, const float* scale, int32_t M,
@@ -70,11 +139,24 @@ inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_
   if ((st = check_codes(q, ldq, w->K)) != BQ_OK) return st;
   if ((st = check_values(y, y_type, ldy, w->N)) != BQ_OK) return st;
   if (!scale || !aligned(scale, 4) || (grouped && (!offsets || !aligned(offsets, 4)))) return BQ_ERR_INVALID_ARG;
+  const SgPlan p = plan_scaled_gemm(M, w->experts, grouped);
+  const int channels = kSgRows * p.cg;
+  const long long tiles = ((long long)(M + p.bn - 1) / p.bn + (grouped ? w->experts : 0)) * ((w->N + channels - 1) / channels);
+  if (tiles > (1 << 30)) return BQ_ERR_SIZE;
   SgArgs a{};
-  a.w = w->codes; a.w_scale = w->scale; a.bias = w->bias; a.q = q; a.scale = scale; a.offsets = offsets; a.y = y;
-  a.ldw = w->ld; a.expert_stride = w->experts > 1 ? w->expert_stride : 0; a.ldq = ldq; a.ldy = ldy;
+  a.w_experts = w->experts > 1 && w->expert_stride > 0 ? w->experts : 1;
+  if (!encode_codes_map(w->codes, w->ld, w->N, w->K, a.w_experts, w->expert_stride, kSgRows, &a.wmap) ||
+      !encode_codes_map(q, ldq, M, w->K, 0, 0, p.bn / p.cg, &a.qmap) ||
+      !encode_codes_map(q, ldq, M, w->K, 0, 0, 16, &a.qmap16))
+    return BQ_ERR_CUDA;
+  a.w_scale = w->scale; a.bias = w->bias; a.scale = scale; a.offsets = offsets; a.y = y; a.ldy = ldy;
   a.M = M; a.N = w->N; a.K = w->K; a.E = w->experts; a.y_type = y_type;
-  return launch_scaled_gemm(a, reinterpret_cast<cudaStream_t>(stream));
+  a.bn = p.bn; a.stages = p.stages; a.stage_bytes = int(kSgWBytes) + p.bn / p.cg * kSgChunk;
+  a.acc_stride = (p.bn + 31) / 32 * 32;
+  a.cols = 32;
+  while (a.cols < 2 * a.acc_stride) a.cols *= 2;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return p.cg == 2 ? launch_scaled_tc<2>(a, p, tiles, s) : launch_scaled_tc<1>(a, p, tiles, s);
 }
 
 }  // namespace bqi
