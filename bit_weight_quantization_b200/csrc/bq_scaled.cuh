@@ -138,20 +138,23 @@ constexpr int kSgCopyWarp = 4, kSgMmaWarp = 5;
 constexpr int kSgMaxStages = 12;
 constexpr int kSgMaxTokens = 256;  // tokens per tile at most
 constexpr uint32_t kSgWBytes = kSgRows * kSgChunk;
-// shared memory: alignment slack, the stages (each a multiple of 1024 bytes), then this region:
+// shared memory: alignment slack, the stages (each a multiple of 1024 bytes), the outputs'
+// staging where y is written by TMA, then this region:
 // full[12] (0), empty[12] (96), acc_full[2] (192), acc_empty[2] (208), words[8] (224), token scales
 // [2][256] (256); then, grouped, the first tile of every expert [E + 1]
+constexpr uint32_t kSgYBytes = 4 * 2 * 2048;  // outputs on their way: two blocks of 32 x 32 for each epilogue warp
 constexpr uint32_t kSgRegion = 256 + 2 * kSgMaxTokens * 4;
 
 struct SgArgs {
   TcTensorMap wmap, qmap, qmap16;  // weights; tokens in boxes of a whole tile, and of 16 rows
+  TcTensorMap ymap;                // 16-bit y in boxes of 32 tokens x 32 channels (y_tma)
   const float* w_scale;
   const float* bias;               // or null
   const float* scale;
   const int* offsets;              // or null: one group of M rows
   void* y;
   long long ldy;
-  int M, N, K, E, y_type;
+  int M, N, K, E, y_type, y_tma;
   int w_experts;                   // distinct weight matrices: E, or 1 where the experts share one
   int bn;                          // tokens per tile at most, a multiple of 16 CG
   int stages, stage_bytes, cols, acc_stride;  // tensor-memory columns, and between accumulators
@@ -226,13 +229,42 @@ __device__ __forceinline__ void sg_arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ float sg_value(uint32_t acc, float s, float b, bool bias) {
-  const float v = float(int(acc));
-  return bias ? __fmaf_rn(v, s, b) : __fmul_rn(v, s);
-}
 __device__ __forceinline__ void sg_put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void sg_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void sg_put(__half* p, float v) { *p = __float2half_rn(v); }
+__device__ __forceinline__ uint32_t sg_pack(__nv_bfloat16, float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t sg_pack(__half, float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// 16 lanes x 32 columns of tensor memory in the m16n8 fragment pattern: thread 4g + t takes columns
+// 8i + 2t and + 1 of lane g in v[4i], v[4i + 1], and of lane g + 8 in v[4i + 2], v[4i + 3]
+__device__ __forceinline__ void sg_ld_fragments(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void sg_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+// four transposed 8x8 blocks of 16-bit values: thread 4g + t holds rows 2t, 2t + 1 of column g of
+// each, lane l gives the address of row l % 8 of block l / 8
+__device__ __forceinline__ void sg_store_blocks(uint32_t saddr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(saddr), "r"(r0),
+               "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
+__device__ __forceinline__ void sg_store_2d(const TcTensorMap* map, int x, int y, uint32_t saddr) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(saddr)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+}
 
 // One tile of work: tokens m0 .. m0 + n - 1 of expert e against the channels from n0 on.
 struct SgTile {
@@ -301,22 +333,81 @@ __device__ __forceinline__ void sg_first_tiles(const SgArgs& a, int* first, int 
   }
 }
 
-// This warp's 32 channels of a tile: tensor-memory lanes to y, column by column (a token's 32
-// channels are one 64- or 128-byte store).
-template <typename Y>
-__device__ __forceinline__ void sg_epilogue(const SgArgs& a, const SgTile& t, uint32_t acc, const float* tok, int n,
-                                            float sw, float b) {
-  Y* y = static_cast<Y*>(a.y) + (long long)t.m0 * a.ldy + n;
-  const bool bias = a.bias != nullptr, live = n < a.N;
-  for (int c = 0; c < t.n; c += 32) {
-    uint32_t v[32];
-    tc_ld32(acc + uint32_t(c), v);
-    if (live) {
+// y of a tile's tokens for this warp's 32 channels ch .. ch + 31 (ch + lane is the thread's). Whole
+// blocks of 32 tokens of 16-bit outputs whose rows are aligned go through shared memory: fragments
+// out of tensor memory, transposed by stmatrix into [token][32 channels] and written by TMA (which
+// drops channels past N), 3.6 instructions an output. The rest (32-bit outputs, unaligned rows, the
+// last tokens) is stored column by column, a token's 32 channels as one 64- or 128-byte store.
+template <typename Y, bool BIAS>
+__device__ __forceinline__ void sg_epilogue(const SgArgs& a, const SgTile& t, uint32_t acc, const float* tok,
+                                            uint8_t* stage, int ch, int lane, int* turn) {
+  const float* ws = a.w_scale + (long long)t.e * a.N;
+  const float* wb = a.bias + (long long)t.e * a.N;
+  int c = 0;
+  if constexpr (sizeof(Y) == 2) {
+    // a store box that N cuts is cut on 16-byte units only: with other N the last channels go below
+    if (a.y_tma && ch < a.N && t.n >= 32 && (ch + 32 <= a.N || a.N % 8 == 0)) {
+      const int g = lane >> 2, tt = lane & 3;
+      float sw[4], b[4];
 #pragma unroll
-      for (int i = 0; i < 32; i++)
-        if (c + i < t.n) sg_put(y + (long long)(c + i) * a.ldy, sg_value(v[i], __fmul_rn(tok[c + i], sw), b, bias));
+      for (int i = 0; i < 4; i++) {
+        const int n = min(ch + 8 * i + g, a.N - 1);
+        sw[i] = __ldg(ws + n);
+        b[i] = BIAS ? __ldg(wb + n) : 0.f;
+      }
+      // row l % 8 of block l / 8, the block's 16 bytes at the 64-byte swizzle's place
+      const uint32_t at = uint32_t(lane & 7) * 64u + (uint32_t(lane >> 3) ^ (uint32_t(lane & 7) >> 1)) * 16u;
+      for (; c + 32 <= t.n; c += 32) {
+        uint32_t lo[16], hi[16];  // channels ch .. + 15, and + 16 .. + 31
+        sg_ld_fragments(acc + uint32_t(c), lo);
+        sg_ld_fragments(acc + (16u << 16) + uint32_t(c), hi);
+        const uint32_t buf = smem_u32(stage) + uint32_t(*turn) * 2048u;
+        *turn ^= 1;
+        // the copy that read this buffer two blocks ago is done
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;\n" ::: "memory");
+        sg_wait_ld();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const float2 s = *reinterpret_cast<const float2*>(tok + c + 8 * i + 2 * tt);
+          uint32_t r[4];
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const uint32_t* v = (j < 2 ? lo : hi) + 4 * i + 2 * (j & 1);
+            const float x0 = float(int(v[0])), x1 = float(int(v[1])), s0 = __fmul_rn(s.x, sw[j]), s1 = __fmul_rn(s.y, sw[j]);
+            r[j] = BIAS ? sg_pack(Y(), __fmaf_rn(x0, s0, b[j]), __fmaf_rn(x1, s1, b[j]))
+                        : sg_pack(Y(), __fmul_rn(x0, s0), __fmul_rn(x1, s1));
+          }
+          sg_store_blocks(buf + uint32_t(i) * 512u + at, r[0], r[1], r[2], r[3]);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) sg_store_2d(&a.ymap, ch, t.m0 + c, buf);
+      }
     }
   }
+  const int n = ch + lane;
+  const bool live = n < a.N;
+  const float sw = live ? __ldg(ws + n) : 0.f, b = BIAS && live ? __ldg(wb + n) : 0.f;
+  Y* y = static_cast<Y*>(a.y) + (t.m0 + c) * a.ldy + n;
+  for (; c < t.n; c += 32) {
+    uint32_t v[32];
+    tc_ld32(acc + uint32_t(c), v);
+    const int left = live ? t.n - c : 0;
+#pragma unroll
+    for (int i = 0; i < 32; i++) {
+      const float x = float(int(v[i])), s = __fmul_rn(tok[c + i], sw);
+      if (i < left) sg_put(y, BIAS ? __fmaf_rn(x, s, b) : __fmul_rn(x, s));
+      y += a.ldy;
+    }
+  }
+}
+
+template <typename Y>
+__device__ __forceinline__ void sg_epilogue(const SgArgs& a, const SgTile& t, uint32_t acc, const float* tok,
+                                            uint8_t* stage, int ch, int lane, int* turn) {
+  if (a.bias) sg_epilogue<Y, true>(a, t, acc, tok, stage, ch, lane, turn);
+  else sg_epilogue<Y, false>(a, t, acc, tok, stage, ch, lane, turn);
 }
 
 template <int CG>
@@ -324,7 +415,7 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
   extern __shared__ __align__(128) uint8_t sg_smem[];
   const uint32_t pad = (1024u - (smem_u32(sg_smem) & 1023u)) & 1023u;
   uint8_t* stages = sg_smem + pad;
-  uint8_t* region = stages + size_t(a.stages) * a.stage_bytes;
+  uint8_t* region = stages + size_t(a.stages) * a.stage_bytes + (a.y_tma ? kSgYBytes : 0u);
   uint64_t* full = reinterpret_cast<uint64_t*>(region);
   uint64_t* empty = full + kSgMaxStages;
   uint64_t* acc_full = empty + kSgMaxStages;
@@ -425,8 +516,10 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
           tc_fence_after();
           const uint32_t wa = smem_u32(stages + size_t(st) * a.stage_bytes);
           const uint64_t da = sg_desc(wa), db = sg_desc(wa + kSgWBytes);
-          const int pieces = min(4, (a.K - k * kSgChunk + 31) / 32);
-          for (int j = 0; j < pieces; j++) sg_mma<CG>(d, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
+          // always the whole chunk (k past K reads as zero): four MMAs of 32 k issued back to back. With
+          // a loop over the pieces that K leaves, the issue alone took 219 cycles an MMA instead of 128
+#pragma unroll
+          for (int j = 0; j < kSgChunk / 32; j++) sg_mma<CG>(d, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
           sg_commit<CG>(&empty[st], 3u);
           if (++st == S) { st = 0; ph ^= 1; }
         }
@@ -437,22 +530,21 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
   } else {
     bool ok = true;
     const uint32_t lanes = uint32_t(32 * warp) << 16;
-    int i = 0;
+    uint8_t* ystage = stages + size_t(S) * a.stage_bytes + warp * 4096;
+    int i = 0, turn = 0;
     for (int u = unit; walk.at(u, &t); u += units, i++) {
       const int buf = i & 1;
       float* tk = tok + buf * kSgMaxTokens;
       for (int j = tid; j < t.n; j += 128) tk[j] = __ldg(a.scale + t.m0 + j);
-      const int n = t.n0 + int(rank) * kSgRows + tid;
-      const long long wn = (long long)t.e * a.N + n;
-      const float sw = n < a.N ? __ldg(a.w_scale + wn) : 0.f, b = a.bias && n < a.N ? __ldg(a.bias + wn) : 0.f;
+      const int ch = t.n0 + int(rank) * kSgRows + 32 * warp;
       asm volatile("bar.sync 1, 128;\n" ::: "memory");  // the scales are written (buffer i - 2 was read before tile i - 1's)
       ok = __all_sync(0xffffffffu, tc_wait(&acc_full[buf], uint32_t((i >> 1) & 1), stop));
       if (ok) {
         tc_fence_after();
         const uint32_t acc = tmem + lanes + uint32_t(buf * a.acc_stride);
-        if (a.y_type == BQ_TYPE_F32) sg_epilogue<float>(a, t, acc, tk, n, sw, b);
-        else if (a.y_type == BQ_TYPE_BF16) sg_epilogue<__nv_bfloat16>(a, t, acc, tk, n, sw, b);
-        else sg_epilogue<__half>(a, t, acc, tk, n, sw, b);
+        if (a.y_type == BQ_TYPE_F32) sg_epilogue<float>(a, t, acc, tk, ystage, ch, lane, &turn);
+        else if (a.y_type == BQ_TYPE_BF16) sg_epilogue<__nv_bfloat16>(a, t, acc, tk, ystage, ch, lane, &turn);
+        else sg_epilogue<__half>(a, t, acc, tk, ystage, ch, lane, &turn);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -464,6 +556,7 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
       }
       // a warp that gave up still takes the tiles' barriers with the others, without waiting for MMAs
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
   }
   __syncthreads();
   if (tid == 0) {

@@ -69,12 +69,28 @@ inline bool encode_codes_map(const int8_t* p, int64_t ld, int64_t rows, int K, i
   return true;
 }
 
+// 16-bit y [M][N] as a TMA map for stores of 32 x 32 blocks (64-byte rows, 64-byte swizzle)
+inline bool encode_output_map(void* y, int64_t ldy, int M, int N, TcTensorMap* out) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {cuuint64_t(N), cuuint64_t(M)};
+  const cuuint64_t strides[1] = {cuuint64_t(ldy) * 2};
+  const cuuint32_t box[2] = {32u, 32u};
+  const cuuint32_t estr[2] = {1u, 1u};
+  CUtensorMap m;
+  if (encode(&m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  std::memcpy(out, &m, sizeof(m));
+  return true;
+}
+
 struct SgPlan {
   int cg, bn, stages;
   uint32_t smem;
 };
 
-inline SgPlan plan_scaled_gemm(int M, int E, bool grouped) {
+inline SgPlan plan_scaled_gemm(int M, int E, bool grouped, bool y_tma) {
   SgPlan p{};
   const long long rows = grouped ? ((long long)M + E - 1) / E : M;  // of one expert, on average
   const long long most = grouped ? std::min<long long>(M, 2 * rows) : M;
@@ -86,7 +102,7 @@ inline SgPlan plan_scaled_gemm(int M, int E, bool grouped) {
     p.bn = int(std::min<long long>(256, (most + 31) / 32 * 32));
   }
   const uint32_t stage = kSgWBytes + uint32_t(p.bn / p.cg) * kSgChunk;
-  const uint32_t fixed = 1024 + kSgRegion + (grouped ? 4u * uint32_t(E + 1) : 0u);
+  const uint32_t fixed = 1024 + kSgRegion + (y_tma ? kSgYBytes : 0u) + (grouped ? 4u * uint32_t(E + 1) : 0u);
   p.stages = std::min(kSgMaxStages, int((kTcSmemMax - fixed) / stage));
   p.smem = fixed + uint32_t(p.stages) * stage;
   return p;
@@ -139,7 +155,9 @@ inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_
   if ((st = check_codes(q, ldq, w->K)) != BQ_OK) return st;
   if ((st = check_values(y, y_type, ldy, w->N)) != BQ_OK) return st;
   if (!scale || !aligned(scale, 4) || (grouped && (!offsets || !aligned(offsets, 4)))) return BQ_ERR_INVALID_ARG;
-  const SgPlan p = plan_scaled_gemm(M, w->experts, grouped);
+  // 16-bit outputs leave by TMA where their rows start on 16-byte boundaries
+  const bool y_tma = y_type != BQ_TYPE_F32 && rows_aligned(y, y_type, ldy);
+  const SgPlan p = plan_scaled_gemm(M, w->experts, grouped, y_tma);
   const int channels = kSgRows * p.cg;
   const long long tiles = ((long long)(M + p.bn - 1) / p.bn + (grouped ? w->experts : 0)) * ((w->N + channels - 1) / channels);
   if (tiles > (1 << 30)) return BQ_ERR_SIZE;
@@ -147,10 +165,10 @@ inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_
   a.w_experts = w->experts > 1 && w->expert_stride > 0 ? w->experts : 1;
   if (!encode_codes_map(w->codes, w->ld, w->N, w->K, a.w_experts, w->expert_stride, kSgRows, &a.wmap) ||
       !encode_codes_map(q, ldq, M, w->K, 0, 0, p.bn / p.cg, &a.qmap) ||
-      !encode_codes_map(q, ldq, M, w->K, 0, 0, 16, &a.qmap16))
+      !encode_codes_map(q, ldq, M, w->K, 0, 0, 16, &a.qmap16) || (y_tma && !encode_output_map(y, ldy, M, w->N, &a.ymap)))
     return BQ_ERR_CUDA;
   a.w_scale = w->scale; a.bias = w->bias; a.scale = scale; a.offsets = offsets; a.y = y; a.ldy = ldy;
-  a.M = M; a.N = w->N; a.K = w->K; a.E = w->experts; a.y_type = y_type;
+  a.M = M; a.N = w->N; a.K = w->K; a.E = w->experts; a.y_type = y_type; a.y_tma = y_tma;
   a.bn = p.bn; a.stages = p.stages; a.stage_bytes = int(kSgWBytes) + p.bn / p.cg * kSgChunk;
   a.acc_stride = (p.bn + 31) / 32 * 32;
   a.cols = 32;
