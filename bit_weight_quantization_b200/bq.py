@@ -350,182 +350,10 @@ class StepGraph:
         self.graph.replay()
 
 
-# ---------------------------------------------------------------------------------------------------
-# scaled int8 layers on torch tensors
-# ---------------------------------------------------------------------------------------------------
-
-def _types():
-    import torch
-    return {torch.float32: BQ_TYPE_F32, torch.bfloat16: BQ_TYPE_BF16, torch.float16: BQ_TYPE_F16}
-
-
-def _need(ok, where, what):
-    if not ok:
-        raise BQError(BQ_ERR_INVALID_ARG, f"{where}: {what}")
-
-
-class _On:
-    """Makes a tensor's device current, and `stream` (a torch stream) torch's current one, so that outputs
-    and workspaces allocated inside belong to the stream that uses them."""
-
-    def __init__(self, device, stream):
-        import torch
-        self._ctx = [] if torch.cuda.current_device() == device.index else [torch.cuda.device(device)]
-        if stream is not None:
-            _need(isinstance(stream, torch.cuda.Stream) and stream.device == device, "stream",
-                  "a torch.cuda.Stream of the tensors' device")
-            self._ctx.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for c in self._ctx:
-            c.__enter__()
-
-    def __exit__(self, *exc):
-        for c in reversed(self._ctx):
-            c.__exit__(*exc)
-
-
-def _rows_of(t, name, where, K=None, dtypes=None, device=None):
-    """A 2-D CUDA matrix with unit column stride: its row stride in elements."""
-    import torch
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2, where, f"{name} is a 2-D CUDA tensor")
-    _need(dtypes is None or t.dtype in dtypes, where, f"{name} has dtype {t.dtype}")
-    _need(device is None or t.device == device, where, f"{name} is on {t.device}")
-    _need(K is None or t.shape[1] == K, where, f"{name} has {t.shape[1]} columns, not {K}")
-    _need(t.shape[1] <= 1 or t.stride(1) == 1, where, f"{name} has column stride {t.stride(1)}")
-    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
-
-
-def _vector(t, name, where, n, dtype, device):
-    import torch
-    _need(isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.is_contiguous() and
-          t.numel() == n, where, f"{name} is {n} contiguous {dtype} on {device}")
-
-
-def empty_codes(rows: int, K: int, device):
-    """An int8 matrix [rows, K] whose rows start on 16-byte boundaries."""
-    import torch
-    return torch.empty((rows, (K + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :K]
-
-
-def scaled_quantize(x, gate=None, rows=None, q=None, scale=None, stream=None):
-    """Per-row int8 codes and scales of x [*, K] (f32, bf16 or f16; see bq_scaled_quantize in include/bq.h):
-    of all rows, or with `rows` (int32 [M]) of row rows[i] for every i (negative: an empty slot); with `gate`
-    of x * SiLU(gate). Returns (q [M, K] int8, scale [M] f32), written to `q` and `scale` where given."""
-    import torch
-    where, types = "scaled_quantize", _types()
-    ldx = _rows_of(x, "x", where, dtypes=types)
-    dev, K, ldg = x.device, x.shape[1], 0
-    if gate is not None:
-        ldg = _rows_of(gate, "gate", where, K, (x.dtype,), dev)
-        _need(gate.shape[0] == x.shape[0], where, f"gate has {gate.shape[0]} rows, x {x.shape[0]}")
-    M = x.shape[0]
-    if rows is not None:
-        _need(rows.dim() == 1, where, "rows is 1-D")
-        M = rows.shape[0]
-        _vector(rows, "rows", where, M, torch.int32, dev)
-    with _On(dev, stream):
-        if q is None:
-            q = empty_codes(M, K, dev)
-        else:
-            _rows_of(q, "q", where, K, (torch.int8,), dev)
-            _need(q.shape[0] == M, where, f"q has {q.shape[0]} rows, not {M}")
-        if scale is None:
-            scale = torch.empty(M, dtype=torch.float32, device=dev)
-        else:
-            _vector(scale, "scale", where, M, torch.float32, dev)
-        ldq = q.stride(0) if M > 1 else (K + 15) // 16 * 16
-        bq_scaled_quantize(x, types[x.dtype], ldx, x.shape[0], gate, ldg, rows, M, K, q, ldq, scale)
-    return q, scale
-
-
-class ScaledLinear:
-    """A layer (or one per expert) of int8 codes [N, K] (or [E, N, K]) with a scale per output channel.
-
-    Holds references to the tensors it is given; `codes` whose rows do not start on 16-byte boundaries
-    are copied once into rows that do. Nothing is kept between calls: outputs and workspaces are
-    allocated per call on the stream that runs it (or given, `y`), so calls on several streams and
-    several captured graphs do not share memory."""
-
-    def __init__(self, codes, scale, bias=None):
-        import torch
-        where = "ScaledLinear"
-        _need(codes.is_cuda and codes.dtype == torch.int8 and codes.dim() in (2, 3) and min(codes.shape) >= 1, where,
-              "codes is a CUDA int8 tensor [N, K] or [E, N, K]")
-        c3 = codes if codes.dim() == 3 else codes[None]
-        E, N, K = c3.shape
-        se, sn, sk = c3.stride()
-        sn, se = (sn if N > 1 else (K + 15) // 16 * 16), (se if E > 1 else 0)
-        if (sk != 1 and K > 1) or sn % 16 or sn < K or se % 16 or se < 0 or c3.data_ptr() % 16:
-            buf = torch.zeros((E, N, (K + 15) // 16 * 16), dtype=torch.int8, device=codes.device)
-            buf[:, :, :K] = c3
-            c3 = buf[:, :, :K]
-            sn, se = buf.stride(1), buf.stride(0)
-        _vector(scale, "scale", where, E * N, torch.float32, codes.device)
-        if bias is not None:
-            _vector(bias, "bias", where, E * N, torch.float32, codes.device)
-        self.codes, self.scale, self.bias, self.device = c3, scale, bias, codes.device
-        self.experts, self.N, self.K = E, N, K
-        self.grouped = codes.dim() == 3
-        self.weights = bq_scaled_weights(c3.data_ptr(), scale.data_ptr(), _ptr(bias), sn, se, N, K, E)
-
-    @classmethod
-    def quantize(cls, W, bias=None):
-        """Codes and scales of W [N, K] or [E, N, K] (f32, bf16 or f16), one scale per output channel."""
-        q, s = scaled_quantize(W.reshape(-1, W.shape[-1]))
-        ld = q.stride(0) if q.shape[0] > 1 else (W.shape[-1] + 15) // 16 * 16
-        q = q.as_strided(W.shape, (W.shape[-2] * ld, ld, 1)[-W.dim():])
-        return cls(q, s.view(W.shape[:-1]), bias)
-
-    def _out(self, y, M, dtype, where):
-        import torch
-        if y is None:
-            return torch.empty((M, self.N), dtype=dtype, device=self.device), self.N
-        ldy = _rows_of(y, "y", where, self.N, _types(), self.device)
-        _need(y.shape[0] == M and (dtype is None or y.dtype == dtype), where, f"y is {M} rows of {dtype or y.dtype}")
-        return y, ldy
-
-    def _codes_in(self, q, scale, where):
-        import torch
-        _rows_of(q, "q", where, self.K, (torch.int8,), self.device)
-        M = q.shape[0]
-        _vector(scale, "scale", where, M, torch.float32, self.device)
-        return M, q.stride(0) if M > 1 else (self.K + 15) // 16 * 16
-
-    def linear(self, x, y=None, dtype=None, stream=None):
-        """x [M, K] (f32, bf16 or f16) quantized per token, then the layer: y [M, N] of `dtype` (x's by default)."""
-        import torch
-        where, types = "ScaledLinear.linear", _types()
-        ldx = _rows_of(x, "x", where, self.K, types, self.device)
-        M = x.shape[0]
-        with _On(self.device, stream):
-            y, ldy = self._out(y, M, dtype if y is not None else dtype or x.dtype, where)
-            _need(y.dtype in types, where, f"y has dtype {y.dtype}")
-            n = bq_scaled_workspace_bytes(self.weights, M)
-            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-            bq_scaled_linear(self.weights, x, types[x.dtype], ldx, M, y, types[y.dtype], ldy, ws, n)
-        return y
-
-    def gemm(self, q, scale, y=None, dtype=None, stream=None):
-        """The layer on quantized rows (scaled_quantize): y [M, N] of `dtype` (bf16 by default)."""
-        import torch
-        where, types = "ScaledLinear.gemm", _types()
-        M, ldq = self._codes_in(q, scale, where)
-        with _On(self.device, stream):
-            y, ldy = self._out(y, M, dtype if y is not None else dtype or torch.bfloat16, where)
-            _need(y.dtype in types, where, f"y has dtype {y.dtype}")
-            bq_scaled_gemm(self.weights, q, ldq, scale, M, y, types[y.dtype], ldy)
-        return y
-
-    def gemm_grouped(self, q, scale, offsets, y=None, dtype=None, stream=None):
-        """Expert e's layer on the rows offsets[e] .. offsets[e + 1] - 1 (offsets: int32 [E + 1] on the device).
-        Rows outside every group keep what `y` held (undefined in a `y` that is allocated here)."""
-        import torch
-        where, types = "ScaledLinear.gemm_grouped", _types()
-        M, ldq = self._codes_in(q, scale, where)
-        _vector(offsets, "offsets", where, self.experts + 1, torch.int32, self.device)
-        with _On(self.device, stream):
-            y, ldy = self._out(y, M, dtype if y is not None else dtype or torch.bfloat16, where)
-            _need(y.dtype in types, where, f"y has dtype {y.dtype}")
-            bq_scaled_gemm_grouped(self.weights, q, ldq, scale, M, offsets, y, types[y.dtype], ldy)
-        return y
+def __getattr__(name: str):
+    # the torch-level scaled int8 layers live in scaled.py, which imports torch (this module does not)
+    if name in ("ScaledLinear", "scaled_quantize", "empty_codes"):
+        from . import scaled
+        globals()[name] = getattr(scaled, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

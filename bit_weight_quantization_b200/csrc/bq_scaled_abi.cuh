@@ -42,12 +42,29 @@ inline bool rows_aligned(const void* p, int type, int64_t ld) {
   return aligned(p, 16) && ld * type_bytes(type) % 16 == 0;
 }
 
+// Threads per row and runs of 8 elements a thread: few rows are spread over as many threads as there
+// are runs (shortest time to the maximum), many rows take up to four runs a thread (fewer idle lanes
+// in the reduction, more bytes in flight a thread).
+template <typename T, bool GATE>
+inline cudaError_t launch_scaled_quantize(SqArgs a, cudaStream_t s) {
+  const int runs = (a.K + 7) / 8;
+  const int c = runs > 4096 ? 0 : runs <= 1024 && ((long long)a.M * runs <= 148 * 1024 || runs <= 64) ? 1 : runs <= 512 ? 2 : 4;
+  if (c == 0) {
+    k_scaled_quantize_long<T, GATE><<<unsigned(a.M), 1024, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  a.per_row = ((runs + c - 1) / c + 31) / 32 * 32;
+  const int rows = std::max(1, 256 / a.per_row);
+  const dim3 grid(unsigned((a.M + (long long)rows - 1) / rows)), block(unsigned(rows * a.per_row));
+  if (c == 1) k_scaled_quantize<T, GATE, 1><<<grid, block, 0, s>>>(a);
+  else if (c == 2) k_scaled_quantize<T, GATE, 2><<<grid, block, 0, s>>>(a);
+  else k_scaled_quantize<T, GATE, 4><<<grid, block, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T>
 inline cudaError_t launch_scaled_quantize(const SqArgs& a, cudaStream_t s) {
-  const dim3 grid(unsigned(std::min(a.M, 148 * 8)));
-  if (a.gate) k_scaled_quantize<T, true><<<grid, 256, 0, s>>>(a);
-  else k_scaled_quantize<T, false><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return a.gate ? launch_scaled_quantize<T, true>(a, s) : launch_scaled_quantize<T, false>(a, s);
 }
 
 // Rows of int8 codes as a TMA map with 128-byte swizzle: [experts][rows][K], boxes of 128 bytes by
@@ -109,7 +126,7 @@ inline SgPlan plan_scaled_gemm(int M, int E, bool grouped, bool y_tma) {
 }
 
 template <int CG>
-inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long tiles, cudaStream_t s) {
+inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long tiles, bool after_quantize, cudaStream_t s) {
   auto k = k_scaled_tc<CG>;
   static std::mutex mu;
   static unsigned long long set_ctx = 0;
@@ -129,13 +146,22 @@ inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long ti
   cfg.blockDim = dim3(kSgThreads);
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = unsigned(CG);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  unsigned n = 0;
+  if (CG > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = unsigned(CG);
+    at[n].val.clusterDim.y = 1;
+    at[n++].val.clusterDim.z = 1;
+  }
+  // Only behind this library's own quantization, itself launched without the attribute: everything
+  // before it, the weights' last writer among it, is then complete when this kernel fetches weights.
+  if (after_quantize) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = at;
-  cfg.numAttrs = CG > 1 ? 1 : 0;
+  cfg.numAttrs = n;
   if (cudaLaunchKernelEx(&cfg, k, a) != cudaSuccess) {
     (void)cudaGetLastError();
     return BQ_ERR_CUDA;
@@ -144,8 +170,8 @@ inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long ti
 }
 
 inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_t ldq, const float* scale, int32_t M,
-                             const int32_t* offsets, bool grouped, void* y, int32_t y_type, int64_t ldy,
-                             void* stream) {
+                             const int32_t* offsets, bool grouped, bool after_quantize, void* y, int32_t y_type,
+                             int64_t ldy, void* stream) {
   bq_status st = check_scaled_weights(w);
   if (st != BQ_OK) return st;
   if (!grouped && w->experts != 1) return BQ_ERR_INVALID_ARG;
@@ -174,7 +200,7 @@ inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_
   a.cols = 32;
   while (a.cols < 2 * a.acc_stride) a.cols *= 2;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return p.cg == 2 ? launch_scaled_tc<2>(a, p, tiles, s) : launch_scaled_tc<1>(a, p, tiles, s);
+  return p.cg == 2 ? launch_scaled_tc<2>(a, p, tiles, after_quantize, s) : launch_scaled_tc<1>(a, p, tiles, after_quantize, s);
 }
 
 }  // namespace bqi
@@ -209,13 +235,13 @@ bq_status bq_scaled_quantize(const void* x, int32_t x_type, int64_t ldx, int32_t
 
 bq_status bq_scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_t ldq, const float* scale, int32_t M,
                          void* y, int32_t y_type, int64_t ldy, void* stream) {
-  return scaled_gemm(w, q, ldq, scale, M, nullptr, false, y, y_type, ldy, stream);
+  return scaled_gemm(w, q, ldq, scale, M, nullptr, false, false, y, y_type, ldy, stream);
 }
 
 bq_status bq_scaled_gemm_grouped(const bq_scaled_weights* w, const int8_t* q, int64_t ldq, const float* scale,
                                  int32_t M, const int32_t* offsets, void* y, int32_t y_type, int64_t ldy,
                                  void* stream) {
-  return scaled_gemm(w, q, ldq, scale, M, offsets, true, y, y_type, ldy, stream);
+  return scaled_gemm(w, q, ldq, scale, M, offsets, true, false, y, y_type, ldy, stream);
 }
 
 bq_status bq_scaled_workspace_bytes(const bq_scaled_weights* w, int32_t M, size_t* bytes) {
@@ -243,7 +269,7 @@ bq_status bq_scaled_linear(const bq_scaled_weights* w, const void* x, int32_t x_
   int8_t* q = static_cast<int8_t*>(workspace);
   float* scale = reinterpret_cast<float*>(q + align256(uint64_t(M) * ld));
   st = bq_scaled_quantize(x, x_type, ldx, M, nullptr, 0, nullptr, M, w->K, q, ld, scale, stream);
-  return st != BQ_OK ? st : bq_scaled_gemm(w, q, ld, scale, M, y, y_type, ldy, stream);
+  return st != BQ_OK ? st : scaled_gemm(w, q, ld, scale, M, nullptr, false, true, y, y_type, ldy, stream);
 }
 
 }  // extern "C"
