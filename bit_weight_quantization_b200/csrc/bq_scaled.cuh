@@ -4,6 +4,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "bq_tc.cuh"
 
 namespace bqi {
@@ -23,48 +25,102 @@ struct SqArgs {
   long long ldx, ldg, ldq;
   int x_rows, M, K;
   int vec_x, vec_g;     // rows of x / gate start on 16-byte boundaries
-  int per_row;          // threads per row, a multiple of 32
 };
 
-__device__ __forceinline__ float sq_to_float(float v) { return v; }
-__device__ __forceinline__ float sq_to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float sq_to_float(__half v) { return __half2float(v); }
-
-// v[0..7] = p[k..k+7] as floats, zero from K on; vec: p is 16-byte aligned (k is a multiple of 8)
+// Eight elements of a row as they lie in memory (zero from K on), their largest |.|, and their
+// values. The order of the bits of |.| is that of the values in all three types, with infinities and
+// then NaNs above, so the maximum is taken on the bits, two 16-bit elements at a time.
 template <typename T>
-__device__ __forceinline__ void sq_load8(const T* p, int k, int K, bool vec, float (&v)[8]) {
-  if (vec && k + 8 <= K) {
-    constexpr int W = int(sizeof(T)) / 2;  // 16-byte words of eight elements: 1 or 2
-    uint4 w[W];
+struct SqRun {
+  static constexpr int W = int(sizeof(T)) * 2;  // 32-bit words
+  uint32_t w[W];
+  // vec: p is 16-byte aligned (k is a multiple of 8)
+  __device__ __forceinline__ void load(const T* p, int k, int K, bool vec) {
+    if (vec && k + 8 <= K) {
 #pragma unroll
-    for (int i = 0; i < W; i++) w[i] = __ldg(reinterpret_cast<const uint4*>(p + k) + i);
-    T t[8];
-    memcpy(t, w, sizeof(t));
+      for (int i = 0; i < W / 4; i++) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + k) + i);
+        w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+      }
+    } else {
+      zero();
 #pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = sq_to_float(t[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = k + i < K ? sq_to_float(p[k + i]) : 0.f;
+      for (int i = 0; i < 8; i++) {
+        if (k + i < K) {
+          if constexpr (sizeof(T) == 4) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + k + i);
+          else w[i >> 1] |= uint32_t(__ldg(reinterpret_cast<const unsigned short*>(p) + k + i)) << (16 * (i & 1));
+        }
+      }
+    }
   }
-}
-
-// the quantized values of row r at k .. k + 7
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < W; i++) w[i] = 0u;
+  }
+  __device__ __forceinline__ uint32_t most(uint32_t m) const {  // of packed |.| bits
+#pragma unroll
+    for (int i = 0; i < W; i++) m = sizeof(T) == 4 ? max(m, w[i] & 0x7FFFFFFFu) : __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    return m;
+  }
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      return __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
+    else return __half2float(__ushort_as_half((unsigned short)(w[i >> 1] >> (16 * (i & 1)))));
+  }
+  // the larger of the packed maxima as the bits of a float
+  static __device__ __forceinline__ uint32_t as_float_bits(uint32_t m) {
+    if constexpr (sizeof(T) == 4) return m;
+    m = max(m & 0xFFFFu, m >> 16);
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) return m << 16;
+    else return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+  }
+};
+// the values of a run times SiLU of another's, kept in f32
+template <>
+struct SqRun<void> {
+  float v[8];
+  template <typename T>
+  __device__ __forceinline__ void load(const SqArgs& a, long long r, int k) {
+    SqRun<T> x, g;
+    x.load(static_cast<const T*>(a.x) + r * a.ldx, k, a.K, a.vec_x != 0);
+    g.load(static_cast<const T*>(a.gate) + r * a.ldg, k, a.K, a.vec_g != 0);
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      v[i] = __fmul_rn(x.value(i), __fdiv_rn(g.value(i), __fadd_rn(1.f, expf(-g.value(i)))));
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = 0.f;
+  }
+  __device__ __forceinline__ uint32_t most(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < 8; i++) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return m;
+  }
+  __device__ __forceinline__ float value(int i) const { return v[i]; }
+  static __device__ __forceinline__ uint32_t as_float_bits(uint32_t m) { return m; }
+};
 template <typename T, bool GATE>
-__device__ __forceinline__ void sq_values(const SqArgs& a, long long r, int k, float (&v)[8]) {
-  sq_load8(static_cast<const T*>(a.x) + r * a.ldx, k, a.K, a.vec_x != 0, v);
-  if constexpr (GATE) {
-    float g[8];
-    sq_load8(static_cast<const T*>(a.gate) + r * a.ldg, k, a.K, a.vec_g != 0, g);
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = __fmul_rn(v[i], __fdiv_rn(g[i], __fadd_rn(1.f, expf(-g[i]))));
-  }
+using SqHeld = SqRun<typename std::conditional<GATE, void, T>::type>;
+
+template <typename T, bool GATE>
+__device__ __forceinline__ void sq_load(const SqArgs& a, long long r, int k, SqHeld<T, GATE>& h) {
+  if constexpr (GATE) h.template load<T>(a, r, k);
+  else h.load(static_cast<const T*>(a.x) + r * a.ldx, k, a.K, a.vec_x != 0);
 }
 
-__device__ __forceinline__ void sq_store8(int8_t* p, int k, int K, const float (&v)[8], float s) {
-  uint32_t w[2] = {0u, 0u};
+// Eight codes to p + k. |v s| <= 127 (1 + 2^-22), so adding 1.5 * 2^23 rounds the (already rounded)
+// product to the nearest whole number, ties to even, and leaves its two's complement in the low byte.
+template <typename H>
+__device__ __forceinline__ void sq_store8(int8_t* p, int k, int K, const H& h, float s) {
+  uint32_t c[8];
 #pragma unroll
-  for (int i = 0; i < 8; i++)
-    w[i >> 2] |= (uint32_t(__float2int_rn(__fmul_rn(v[i], s))) & 0xFFu) << (8 * (i & 3));
+  for (int i = 0; i < 8; i++) c[i] = __float_as_uint(__fadd_rn(__fmul_rn(h.value(i), s), 12582912.f));
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; i++)
+    w[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
   if (k + 8 <= K) {
     *reinterpret_cast<uint2*>(p + k) = make_uint2(w[0], w[1]);
   } else {
@@ -72,25 +128,19 @@ __device__ __forceinline__ void sq_store8(int8_t* p, int k, int K, const float (
   }
 }
 
-// What a row's maximum makes of it. m: the largest |v| as bits, in which infinities and NaNs order
-// above every finite value.
+// What a row's maximum makes of it. m: the largest |v| as bits.
 struct SqScale {
-  float s, scale;
-  bool some;
-  __device__ __forceinline__ explicit SqScale(uint32_t m) {
-    const bool fine = m < 0x7F800000u;
-    some = fine && m >= 0x0D800000u;  // 2^-100: 1 / gamma and 127 / gamma stay finite
-    const float gamma = __uint_as_float(m);
-    s = some ? __fmul_rn(127.f, __frcp_rn(gamma)) : 0.f;
-    scale = !fine ? __uint_as_float(0x7FC00000u) : some ? __fdiv_rn(gamma, 127.f) : 0.f;
+  uint32_t m;
+  float s;
+  __device__ __forceinline__ explicit SqScale(uint32_t most) : m(most) {
+    s = some() ? __fmul_rn(127.f, __frcp_rn(__uint_as_float(m))) : 0.f;
+  }
+  __device__ __forceinline__ bool fine() const { return m < 0x7F800000u; }
+  __device__ __forceinline__ bool some() const { return fine() && m >= 0x0D800000u; }  // 2^-100: s is finite
+  __device__ __forceinline__ float scale() const {
+    return !fine() ? __uint_as_float(0x7FC00000u) : some() ? __fdiv_rn(__uint_as_float(m), 127.f) : 0.f;
   }
 };
-
-__device__ __forceinline__ uint32_t sq_max8(uint32_t m, const float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; j++) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  return m;
-}
 
 // A row's slot: its source row, or -1 where it is empty or out of range
 __device__ __forceinline__ int sq_row(const SqArgs& a, int i, bool* bad) {
@@ -101,51 +151,49 @@ __device__ __forceinline__ int sq_row(const SqArgs& a, int i, bool* bad) {
 
 __device__ __forceinline__ void sq_finish(const SqArgs& a, int i, const SqScale& c, bool bad) {
   if (bad) atomicOr(&g_bq_device_error, kErrScaledIndex);
-  a.scale[i] = bad ? __uint_as_float(0x7FC00000u) : c.scale;
+  a.scale[i] = bad ? __uint_as_float(0x7FC00000u) : c.scale();
 }
 
-// A row lies in the registers of `per_row` threads, C runs of 8 elements each, so x is read once and
-// the gate computed once: bound by memory (K = 4096 bf16 gathered: 134 MB through the L2, 67 MB out),
-// with the gate by its exp and divide. A block holds blockDim / per_row rows, whole warps each.
-template <typename T, bool GATE, int C>
-__global__ void __launch_bounds__(1024) k_scaled_quantize(const SqArgs a) {
+// A row lies in the registers of blockDim.x threads (whole warps), C runs of 8 elements each, so x is
+// read once and the gate computed once; blockDim.y rows a block. Bound by memory for f32 and, with 8 runs
+// a thread to spread the fixed cost of a thread over, nearly so for 16-bit types; with the gate by the
+// instruction issue of its exp and divide, for which the registers are held to 40 so that 48 warps fit
+// an SM (60 registers, 22 warps: 95 us for 4096 x 11008 bf16, against 65).
+template <typename T, bool GATE, int C, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_scaled_quantize(const SqArgs a) {
   __shared__ uint32_t most[32];
   pdl_trigger();
-  const int warps = a.per_row >> 5, warp = threadIdx.x >> 5, w0 = warp / warps * warps;
-  const int i = int(blockIdx.x) * int(blockDim.x / a.per_row) + warp / warps;
-  const int col = 8 * (threadIdx.x - 32 * w0);
+  const int i = int(blockIdx.x * blockDim.y + threadIdx.y);
   const bool live = i < a.M;
   bool bad = false;
   const int r = live ? sq_row(a, i, &bad) : -1;
-  float v[C][8];
+  SqHeld<T, GATE> h[C];
   uint32_t m = 0;
 #pragma unroll
   for (int c = 0; c < C; c++) {
-    const int k = col + c * 8 * a.per_row;
-#pragma unroll
-    for (int j = 0; j < 8; j++) v[c][j] = 0.f;
-    if (r >= 0 && k < a.K) sq_values<T, GATE>(a, r, k, v[c]);
+    const int k = 8 * int(threadIdx.x + c * blockDim.x);
+    if (r >= 0 && k < a.K) sq_load<T, GATE>(a, r, k, h[c]);
+    else h[c].zero();
   }
 #pragma unroll
-  for (int c = 0; c < C; c++) m = sq_max8(m, v[c]);
-  m = __reduce_max_sync(0xffffffffu, m);
-  if (warps > 1) {
-    if ((threadIdx.x & 31) == 0) most[warp] = m;
+  for (int c = 0; c < C; c++) m = h[c].most(m);
+  m = __reduce_max_sync(0xffffffffu, SqHeld<T, GATE>::as_float_bits(m));
+  if (blockDim.x > 32) {
+    const int warps = blockDim.x >> 5, w0 = threadIdx.y * warps, lane = threadIdx.x & 31;
+    if (lane == 0) most[w0 + (threadIdx.x >> 5)] = m;
     __syncthreads();
-    m = __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < warps ? most[w0 + (threadIdx.x & 31)] : 0u);
+    m = __reduce_max_sync(0xffffffffu, lane < warps ? most[w0 + lane] : 0u);
   }
   if (!live) return;
   const SqScale q(m);
+  int8_t* out = a.q + i * a.ldq;
 #pragma unroll
   for (int c = 0; c < C; c++) {
-    const int k = col + c * 8 * a.per_row;
-    if (!q.some) {  // infinities and NaNs must not meet the conversion
-#pragma unroll
-      for (int j = 0; j < 8; j++) v[c][j] = 0.f;
-    }
-    if (k < a.K) sq_store8(a.q + i * a.ldq, k, a.K, v[c], q.s);
+    const int k = 8 * int(threadIdx.x + c * blockDim.x);
+    if (!q.some()) h[c].zero();  // infinities and NaNs must not meet the rounding
+    if (k < a.K) sq_store8(out, k, a.K, h[c], q.s);
   }
-  if (col == 0) sq_finish(a, i, q, bad);
+  if (threadIdx.x == 0) sq_finish(a, i, q, bad);
 }
 
 // Rows too long for that: one block of 1024 per row, x read twice (the second time from the caches).
@@ -157,21 +205,20 @@ __global__ void __launch_bounds__(1024) k_scaled_quantize_long(const SqArgs a) {
   bool bad;
   const int r = sq_row(a, i, &bad);
   uint32_t m = 0;
-  float v[8];
+  SqHeld<T, GATE> h;
   for (int k = 8 * threadIdx.x; k < a.K && r >= 0; k += 8 * 1024) {
-    sq_values<T, GATE>(a, r, k, v);
-    m = sq_max8(m, v);
+    sq_load<T, GATE>(a, r, k, h);
+    m = h.most(m);
   }
-  m = __reduce_max_sync(0xffffffffu, m);
+  m = __reduce_max_sync(0xffffffffu, SqHeld<T, GATE>::as_float_bits(m));
   if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
   __syncthreads();
   m = __reduce_max_sync(0xffffffffu, most[threadIdx.x & 31]);
   const SqScale q(m);
   for (int k = 8 * threadIdx.x; k < a.K; k += 8 * 1024) {
-#pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = 0.f;
-    if (q.some) sq_values<T, GATE>(a, r, k, v);
-    sq_store8(a.q + i * a.ldq, k, a.K, v, q.s);
+    if (q.some()) sq_load<T, GATE>(a, r, k, h);
+    else h.zero();
+    sq_store8(a.q + i * a.ldq, k, a.K, h, q.s);
   }
   if (threadIdx.x == 0) sq_finish(a, i, q, bad);
 }

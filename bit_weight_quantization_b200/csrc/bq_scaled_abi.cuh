@@ -42,24 +42,36 @@ inline bool rows_aligned(const void* p, int type, int64_t ld) {
   return aligned(p, 16) && ld * type_bytes(type) % 16 == 0;
 }
 
-// Threads per row and runs of 8 elements a thread: few rows are spread over as many threads as there
-// are runs (shortest time to the maximum), many rows take up to four runs a thread (fewer idle lanes
-// in the reduction, more bytes in flight a thread).
+template <typename T, bool GATE, int C, int MAXT, int MINB>
+inline cudaError_t launch_scaled_rows(const SqArgs& a, cudaStream_t s) {
+  const int runs = (a.K + 7) / 8, per_row = ((runs + C - 1) / C + 31) / 32 * 32, rows = std::max(1, 256 / per_row);
+  k_scaled_quantize<T, GATE, C, MAXT, MINB>
+      <<<unsigned((a.M + (long long)rows - 1) / rows), dim3(unsigned(per_row), unsigned(rows)), 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+// Runs of 8 elements a thread. Few rows are spread over as many threads as they fill (64 rows of 11008
+// bf16: 2.7 us with two runs a thread, 3.3 with eight). Many rows take four, or eight where a run is
+// four registers (16384 rows of 4096 bf16, gathered: 64 / 41 / 33 us with one, two and eight).
 template <typename T, bool GATE>
-inline cudaError_t launch_scaled_quantize(SqArgs a, cudaStream_t s) {
+inline cudaError_t launch_scaled_quantize(const SqArgs& a, cudaStream_t s) {
   const int runs = (a.K + 7) / 8;
-  const int c = runs > 4096 ? 0 : runs <= 1024 && ((long long)a.M * runs <= 148 * 1024 || runs <= 64) ? 1 : runs <= 512 ? 2 : 4;
-  if (c == 0) {
+  if (runs > 4096) {
     k_scaled_quantize_long<T, GATE><<<unsigned(a.M), 1024, 0, s>>>(a);
     return cudaGetLastError();
   }
-  a.per_row = ((runs + c - 1) / c + 31) / 32 * 32;
-  const int rows = std::max(1, 256 / a.per_row);
-  const dim3 grid(unsigned((a.M + (long long)rows - 1) / rows)), block(unsigned(rows * a.per_row));
-  if (c == 1) k_scaled_quantize<T, GATE, 1><<<grid, block, 0, s>>>(a);
-  else if (c == 2) k_scaled_quantize<T, GATE, 2><<<grid, block, 0, s>>>(a);
-  else k_scaled_quantize<T, GATE, 4><<<grid, block, 0, s>>>(a);
-  return cudaGetLastError();
+  if ((long long)a.M * runs <= 148 * 1024 || runs <= 64) {
+    if (runs <= 1024) return launch_scaled_rows<T, GATE, 1, 1024, 1>(a, s);
+    if (runs <= 2048) return launch_scaled_rows<T, GATE, 2, 1024, 1>(a, s);
+    return launch_scaled_rows<T, GATE, 4, 1024, 1>(a, s);
+  }
+  if (runs <= 128) return launch_scaled_rows<T, GATE, 2, 256, 1>(a, s);
+  if constexpr (!GATE && sizeof(T) == 2)
+    return launch_scaled_rows<T, GATE, 8, 512, 2>(a, s);
+  else if (runs > 2048)
+    return launch_scaled_rows<T, GATE, 4, 1024, 1>(a, s);
+  else
+    return launch_scaled_rows<T, GATE, 4, 512, GATE ? 3 : 2>(a, s);
 }
 
 template <typename T>
