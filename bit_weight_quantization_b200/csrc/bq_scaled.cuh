@@ -707,4 +707,149 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
   }
 }
 
+// ---------------------------------------------------------------------------
+// one to eight tokens
+// ---------------------------------------------------------------------------
+//
+// For a few tokens the product is a pass over the weights, N K bytes, and the tensor cores are idle
+// weight: a warp takes R channels at a time with 16-byte loads, each used for every token through
+// 4-byte dot products against the tokens' codes in shared memory. One launch serves
+// bq_scaled_linear too: every block quantizes the tokens itself (they are a few KB) while its first
+// weights are on their way.
+
+constexpr int kSvThreads = 256;
+constexpr int kSvMaxTokens = 8;
+constexpr int kSvMaxCodes = 96 * 1024;  // bytes of codes in shared memory
+
+struct SvArgs {
+  SqArgs x;             // the tokens (rows, gate unused); for codes, x.q and x.scale are read
+  const int8_t* w;
+  const float* w_scale;
+  const float* bias;    // or null
+  void* y;
+  long long ldw, ldy;
+  int M, N, K, y_type;
+};
+
+// 16 codes of a row from k on; the bytes from K on are not read
+__device__ __forceinline__ uint4 sv_codes(const int8_t* row, int k, int K) {
+  if (k + 16 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  for (int i = 0; k + i < K; i++) w[i >> 2] |= uint32_t(uint8_t(__ldg(row + k + i))) << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The tokens' codes [TOK][Kp] and scales into shared memory. T = int8_t: copied; else quantized as
+// k_scaled_quantize does.
+template <typename T, int TOK>
+__device__ __forceinline__ void sv_stage(const SvArgs& a, int8_t* codes, float* scale, uint32_t* most, int Kp) {
+  const int tid = threadIdx.x;
+  if constexpr (std::is_same<T, int8_t>::value) {
+    for (int i = 16 * tid; i < TOK * Kp; i += 16 * kSvThreads) {
+      const int t = i / Kp, k = i - t * Kp;
+      *reinterpret_cast<uint4*>(codes + i) =
+          t < a.M && k < a.K ? sv_codes(a.x.q + t * a.x.ldq, k, a.K) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (tid < TOK) scale[tid] = tid < a.M ? a.x.scale[tid] : 0.f;
+    __syncthreads();
+  } else {
+    uint32_t m[TOK];
+#pragma unroll
+    for (int t = 0; t < TOK; t++) {
+      m[t] = 0u;
+      if (t < a.M) {
+        for (int k = 8 * tid; k < a.K; k += 8 * kSvThreads) {
+          SqRun<T> h;
+          h.load(static_cast<const T*>(a.x.x) + t * a.x.ldx, k, a.K, a.x.vec_x != 0);
+          m[t] = h.most(m[t]);
+        }
+      }
+      m[t] = __reduce_max_sync(0xffffffffu, SqRun<T>::as_float_bits(m[t]));
+      if ((tid & 31) == 0) most[8 * t + (tid >> 5)] = m[t];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < TOK; t++) {
+      const SqScale q(__reduce_max_sync(0xffffffffu, most[8 * t + (tid & 7)]));
+      if (tid == 0) scale[t] = q.scale();
+      for (int k = 8 * tid; k < Kp; k += 8 * kSvThreads) {
+        SqRun<T> h;
+        if (t < a.M && k < a.K && q.some()) h.load(static_cast<const T*>(a.x.x) + t * a.x.ldx, k, a.K, a.x.vec_x != 0);
+        else h.zero();
+        sq_store8(codes + t * Kp, k, Kp, h, q.s);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, int TOK, int R>
+__global__ void __launch_bounds__(kSvThreads, 2) k_scaled_gemv(const SvArgs a) {
+  constexpr int U = 8 / R;  // 8 loads of 16 bytes in flight a lane
+  extern __shared__ __align__(16) int8_t sv_codes_smem[];
+  __shared__ uint32_t most[8 * TOK];
+  __shared__ float scale[TOK];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int Kp = (a.K + 511) / 512 * 512, groups = (a.N + R - 1) / R, step = int(gridDim.x) * 8;
+  int g = int(blockIdx.x) * 8 + warp;
+  uint4 w[U][R];
+  auto fetch = [&](int n0, int k0) {
+#pragma unroll
+    for (int u = 0; u < U; u++)
+#pragma unroll
+      for (int r = 0; r < R; r++) {
+        const int k = k0 + 512 * u + 16 * lane;
+        w[u][r] = k < a.K && n0 + r < a.N ? sv_codes(a.w + (long long)(n0 + r) * a.ldw, k, a.K) : make_uint4(0u, 0u, 0u, 0u);
+      }
+  };
+  fetch(min(g, groups - 1) * R, 0);
+  sv_stage<T, TOK>(a, sv_codes_smem, scale, most, Kp);
+  for (; g < groups; g += step) {
+    const int n0 = g * R;
+    int acc[R][TOK] = {};
+    for (int k0 = 0; k0 < Kp; k0 += 512 * U) {
+      uint4 v[U][R];
+#pragma unroll
+      for (int u = 0; u < U; u++)
+#pragma unroll
+        for (int r = 0; r < R; r++) v[u][r] = w[u][r];
+      if (k0 + 512 * U < Kp) fetch(n0, k0 + 512 * U);
+      else if (g + step < groups) fetch((g + step) * R, 0);
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        if (k0 + 512 * u < Kp) {
+#pragma unroll
+          for (int t = 0; t < TOK; t++) {
+            const int4 x = *reinterpret_cast<const int4*>(sv_codes_smem + t * Kp + k0 + 512 * u + 16 * lane);
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+              acc[r][t] = __dp4a(int(v[u][r].x), x.x, acc[r][t]);
+              acc[r][t] = __dp4a(int(v[u][r].y), x.y, acc[r][t]);
+              acc[r][t] = __dp4a(int(v[u][r].z), x.z, acc[r][t]);
+              acc[r][t] = __dp4a(int(v[u][r].w), x.w, acc[r][t]);
+            }
+          }
+        }
+      }
+    }
+    int mine = 0;  // lane R t + r: token t, channel n0 + r
+#pragma unroll
+    for (int t = 0; t < TOK; t++)
+#pragma unroll
+      for (int r = 0; r < R; r++) {
+        const int sum = __reduce_add_sync(0xffffffffu, acc[r][t]);
+        if (lane == R * t + r) mine = sum;
+      }
+    const int t = lane / R, n = n0 + lane % R;
+    if (t < a.M && t < TOK && n < a.N) {
+      const float s = __fmul_rn(scale[t], __ldg(a.w_scale + n)), v = float(mine);
+      const float y = a.bias ? __fmaf_rn(v, s, __ldg(a.bias + n)) : __fmul_rn(v, s);
+      const long long at = t * a.ldy + n;
+      if (a.y_type == BQ_TYPE_F32) sg_put(static_cast<float*>(a.y) + at, y);
+      else if (a.y_type == BQ_TYPE_BF16) sg_put(static_cast<__nv_bfloat16*>(a.y) + at, y);
+      else sg_put(static_cast<__half*>(a.y) + at, y);
+    }
+  }
+}
+
 }  // namespace bqi

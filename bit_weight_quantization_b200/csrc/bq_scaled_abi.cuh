@@ -181,6 +181,58 @@ inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long ti
   return BQ_OK;
 }
 
+// One to kSvMaxTokens tokens whose codes fit in shared memory take the pass over the weights.
+inline bool scaled_few_tokens(int M, int K) {
+  const int tok = pow2ceil(M);
+  return M <= kSvMaxTokens && tok * ((K + 511) / 512 * 512) <= kSvMaxCodes;
+}
+
+template <typename T, int TOK, int R>
+inline bq_status launch_scaled_gemv_r(const SvArgs& a, cudaStream_t s) {
+  auto k = k_scaled_gemv<T, TOK, R>;
+  static std::mutex mu;
+  static unsigned long long set_ctx = 0;
+  const unsigned smem = unsigned(TOK * ((a.K + 511) / 512 * 512));
+  if (smem > 40 * 1024) {
+    const unsigned long long ctx = current_context_id();
+    std::lock_guard<std::mutex> lock(mu);
+    if (ctx == 0 || ctx != set_ctx) {
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSvMaxCodes) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return BQ_ERR_CUDA;
+      }
+      set_ctx = ctx;
+    }
+  }
+  const int blocks = std::min(((a.N + R - 1) / R + 7) / 8, 2 * sm_count());
+  k<<<unsigned(blocks), kSvThreads, smem, s>>>(a);
+  return launch_status();
+}
+
+template <typename T, int TOK>
+inline bq_status launch_scaled_gemv_t(const SvArgs& a, cudaStream_t s) {
+  // channels a warp: as many as leave every warp of two blocks an SM a group
+  const int warps = 16 * sm_count();
+  if (a.N >= 4 * warps) return launch_scaled_gemv_r<T, TOK, 4>(a, s);
+  if (a.N >= 2 * warps) return launch_scaled_gemv_r<T, TOK, 2>(a, s);
+  return launch_scaled_gemv_r<T, TOK, 1>(a, s);
+}
+
+template <typename T>
+inline bq_status launch_scaled_gemv(const SvArgs& a, cudaStream_t s) {
+  if (a.M <= 1) return launch_scaled_gemv_t<T, 1>(a, s);
+  if (a.M <= 2) return launch_scaled_gemv_t<T, 2>(a, s);
+  if (a.M <= 4) return launch_scaled_gemv_t<T, 4>(a, s);
+  return launch_scaled_gemv_t<T, 8>(a, s);
+}
+
+inline SvArgs scaled_gemv_args(const bq_scaled_weights* w, int M, void* y, int y_type, int64_t ldy) {
+  SvArgs a{};
+  a.w = w->codes; a.w_scale = w->scale; a.bias = w->bias; a.y = y; a.ldw = w->ld; a.ldy = ldy;
+  a.M = M; a.N = w->N; a.K = w->K; a.y_type = y_type;
+  return a;
+}
+
 inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_t ldq, const float* scale, int32_t M,
                              const int32_t* offsets, bool grouped, bool after_quantize, void* y, int32_t y_type,
                              int64_t ldy, void* stream) {
@@ -193,6 +245,13 @@ inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_
   if ((st = check_codes(q, ldq, w->K)) != BQ_OK) return st;
   if ((st = check_values(y, y_type, ldy, w->N)) != BQ_OK) return st;
   if (!scale || !aligned(scale, 4) || (grouped && (!offsets || !aligned(offsets, 4)))) return BQ_ERR_INVALID_ARG;
+  if (!grouped && scaled_few_tokens(M, w->K)) {
+    SvArgs a = scaled_gemv_args(w, M, y, y_type, ldy);
+    a.x.q = const_cast<int8_t*>(q);
+    a.x.ldq = ldq;
+    a.x.scale = const_cast<float*>(scale);
+    return launch_scaled_gemv<int8_t>(a, reinterpret_cast<cudaStream_t>(stream));
+  }
   // 16-bit outputs leave by TMA where their rows start on 16-byte boundaries
   const bool y_tma = y_type != BQ_TYPE_F32 && rows_aligned(y, y_type, ldy);
   const SgPlan p = plan_scaled_gemm(M, w->experts, grouped, y_tma);
@@ -277,6 +336,16 @@ bq_status bq_scaled_linear(const bq_scaled_weights* w, const void* x, int32_t x_
   if ((st = check_values(y, y_type, ldy, w->N)) != BQ_OK) return st;
   if (!workspace || !aligned(workspace, 256)) return BQ_ERR_INVALID_ARG;
   if (workspace_bytes < need) return BQ_ERR_SIZE;
+  if (scaled_few_tokens(M, w->K)) {
+    SvArgs a = scaled_gemv_args(w, M, y, y_type, ldy);
+    a.x.x = x;
+    a.x.ldx = ldx;
+    a.x.vec_x = rows_aligned(x, x_type, ldx);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return x_type == BQ_TYPE_F32    ? launch_scaled_gemv<float>(a, s)
+           : x_type == BQ_TYPE_BF16 ? launch_scaled_gemv<__nv_bfloat16>(a, s)
+                                    : launch_scaled_gemv<__half>(a, s);
+  }
   const int64_t ld = scaled_ld(w->K);
   int8_t* q = static_cast<int8_t*>(workspace);
   float* scale = reinterpret_cast<float*>(q + align256(uint64_t(M) * ld));
