@@ -708,147 +708,315 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
 }
 
 // ---------------------------------------------------------------------------
-// one to eight tokens
+// few tokens
 // ---------------------------------------------------------------------------
 //
-// For a few tokens the product is a pass over the weights, N K bytes, and the tensor cores are idle
-// weight: a warp takes R channels at a time with 16-byte loads, each used for every token through
-// 4-byte dot products against the tokens' codes in shared memory. One launch serves
-// bq_scaled_linear too: every block quantizes the tokens itself (they are a few KB) while its first
-// weights are on their way.
+// For at most 64 tokens the product is a pass over the weights, N K bytes, and N / 128 tiles are too
+// few for the SMs. So a cluster of CTAs splits the k-range of one 128-channel tile; each leaves its
+// s32 sums in the shared memory of the CTA that finishes those tokens (integer sums: exact in any
+// order). The tensor cores keep up with the memory although an MMA of 128 channels costs the same
+// 43 ns for 16 tokens as for 128 (4 KB of weights: 95 GB/s an SM, 14 TB/s in all).
+//
+// T = int8_t: the tokens' codes come by TMA beside the weights. Otherwise x is quantized here, by
+// every CTA the tokens of the whole row (their maximum) and the codes of its own k-range, straight
+// into the operand's swizzled rows, while the weights are on their way: one launch for a decoded token.
 
-constexpr int kSvThreads = 256;
-constexpr int kSvMaxTokens = 8;
-constexpr int kSvMaxCodes = 96 * 1024;  // bytes of codes in shared memory
+constexpr int kSsMaxTokens = 64, kSsFusedTokens = 4;
+constexpr int kSsMaxSplit = 8;
+constexpr uint32_t kSsFusedRow = 16 * kSgChunk;  // a chunk of the fused operand: 16 rows of 128 codes
+// after the stages, the fused operand and the received sums: full[12] (0), empty[12] (96), acc_full
+// (192), tok_full (200), sums_full (208), words[8] (224), token scales [64] (256), maxima [4][4] (512)
+constexpr uint32_t kSsRegion = 576;
 
-struct SvArgs {
-  SqArgs x;             // the tokens (rows, gate unused); for codes, x.q and x.scale are read
-  const int8_t* w;
+struct SsArgs {
+  TcTensorMap wmap, qmap;  // boxes of 128 channels, and of nn tokens
+  SqArgs x;                // T != int8_t: the unquantized tokens
   const float* w_scale;
-  const float* bias;    // or null
+  const float* bias;       // or null
+  const float* scale;      // T = int8_t: the tokens' scales
   void* y;
-  long long ldw, ldy;
+  long long ldy;
   int M, N, K, y_type;
+  int nn, stages, stage_bytes, cols, splits;
+  int slice;               // tokens that one CTA of the cluster finishes
+  int ahead;               // the kernel before this one is the quantization: weights may be fetched before it ends
 };
 
-// 16 codes of a row from k on; the bytes from K on are not read
-__device__ __forceinline__ uint4 sv_codes(const int8_t* row, int k, int K) {
-  if (k + 16 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-  for (int i = 0; k + i < K; i++) w[i >> 2] |= uint32_t(uint8_t(__ldg(row + k + i))) << (8 * (i & 3));
-  return make_uint4(w[0], w[1], w[2], w[3]);
+// shared memory of this CTA to that of a CTA of the cluster, counted by a barrier there
+__device__ __forceinline__ void dsmem_copy(uint32_t rdst, uint32_t src, uint32_t bytes, uint32_t rbar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(rdst),
+               "r"(src), "r"(bytes), "r"(rbar)
+               : "memory");
+}
+// 32 lanes x 8 columns of tensor memory
+__device__ __forceinline__ void ss_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr)
+               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 }
 
-// The tokens' codes [TOK][Kp] and scales into shared memory. T = int8_t: copied; else quantized as
-// k_scaled_quantize does.
-template <typename T, int TOK>
-__device__ __forceinline__ void sv_stage(const SvArgs& a, int8_t* codes, float* scale, uint32_t* most, int Kp) {
-  const int tid = threadIdx.x;
-  if constexpr (std::is_same<T, int8_t>::value) {
-    for (int i = 16 * tid; i < TOK * Kp; i += 16 * kSvThreads) {
-      const int t = i / Kp, k = i - t * Kp;
-      *reinterpret_cast<uint4*>(codes + i) =
-          t < a.M && k < a.K ? sv_codes(a.x.q + t * a.x.ldq, k, a.K) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    if (tid < TOK) scale[tid] = tid < a.M ? a.x.scale[tid] : 0.f;
-    __syncthreads();
-  } else {
-    uint32_t m[TOK];
+// y of this thread's channel for the tokens m0 .. m1 - 1; sum(m) gives their exact sums, eight of them
+// before the first is used
+template <typename Y, typename F>
+__device__ __forceinline__ void ss_out(const SsArgs& a, int m0, int m1, int n, const float* scale, float sw, float b,
+                                       F sum) {
+  Y* y = static_cast<Y*>(a.y) + m0 * a.ldy + n;
+  for (int m = m0; m < m1; m += 8) {
+    int v[8];
 #pragma unroll
-    for (int t = 0; t < TOK; t++) {
-      m[t] = 0u;
-      if (t < a.M) {
-        for (int k = 8 * tid; k < a.K; k += 8 * kSvThreads) {
-          SqRun<T> h;
-          h.load(static_cast<const T*>(a.x.x) + t * a.x.ldx, k, a.K, a.x.vec_x != 0);
-          m[t] = h.most(m[t]);
-        }
-      }
-      m[t] = __reduce_max_sync(0xffffffffu, SqRun<T>::as_float_bits(m[t]));
-      if ((tid & 31) == 0) most[8 * t + (tid >> 5)] = m[t];
-    }
-    __syncthreads();
+    for (int i = 0; i < 8; i++) v[i] = m + i < m1 ? int(sum(m + i)) : 0;
 #pragma unroll
-    for (int t = 0; t < TOK; t++) {
-      const SqScale q(__reduce_max_sync(0xffffffffu, most[8 * t + (tid & 7)]));
-      if (tid == 0) scale[t] = q.scale();
-      for (int k = 8 * tid; k < Kp; k += 8 * kSvThreads) {
-        SqRun<T> h;
-        if (t < a.M && k < a.K && q.some()) h.load(static_cast<const T*>(a.x.x) + t * a.x.ldx, k, a.K, a.x.vec_x != 0);
-        else h.zero();
-        sq_store8(codes + t * Kp, k, Kp, h, q.s);
+    for (int i = 0; i < 8; i++) {
+      if (m + i < m1) {
+        const float s = __fmul_rn(scale[m + i], sw), f = float(v[i]);
+        sg_put(y, a.bias ? __fmaf_rn(f, s, b) : __fmul_rn(f, s));
+        y += a.ldy;
       }
     }
-    __syncthreads();
+  }
+}
+template <typename F>
+__device__ __forceinline__ void ss_out(const SsArgs& a, int m0, int m1, int n, const float* scale, float sw, float b,
+                                       F sum) {
+  if (a.y_type == BQ_TYPE_F32) ss_out<float>(a, m0, m1, n, scale, sw, b, sum);
+  else if (a.y_type == BQ_TYPE_BF16) ss_out<__nv_bfloat16>(a, m0, m1, n, scale, sw, b, sum);
+  else ss_out<__half>(a, m0, m1, n, scale, sw, b, sum);
+}
+
+// Warps 0-3: every token's largest |x| of this warp's share of the row, to most[4 t + warp].
+template <typename T>
+__device__ __forceinline__ void ss_maxima(const SsArgs& a, uint32_t* most, int tid) {
+  uint32_t m[kSsFusedTokens] = {};
+#pragma unroll 2
+  for (int k = 8 * tid; k < a.K; k += 8 * 128) {
+    SqRun<T> h[kSsFusedTokens];
+#pragma unroll
+    for (int t = 0; t < kSsFusedTokens; t++)
+      if (t < a.M) h[t].load(static_cast<const T*>(a.x.x) + t * a.x.ldx, k, a.K, a.x.vec_x != 0);
+      else h[t].zero();
+#pragma unroll
+    for (int t = 0; t < kSsFusedTokens; t++) m[t] = h[t].most(m[t]);
+  }
+#pragma unroll
+  for (int t = 0; t < kSsFusedTokens; t++) {
+    m[t] = __reduce_max_sync(0xffffffffu, SqRun<T>::as_float_bits(m[t]));
+    if ((tid & 31) == 0) most[4 * t + (tid >> 5)] = m[t];
   }
 }
 
-template <typename T, int TOK, int R>
-__global__ void __launch_bounds__(kSvThreads, 2) k_scaled_gemv(const SvArgs a) {
-  constexpr int U = 8 / R;  // 8 loads of 16 bytes in flight a lane
-  extern __shared__ __align__(16) int8_t sv_codes_smem[];
-  __shared__ uint32_t most[8 * TOK];
-  __shared__ float scale[TOK];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int Kp = (a.K + 511) / 512 * 512, groups = (a.N + R - 1) / R, step = int(gridDim.x) * 8;
-  int g = int(blockIdx.x) * 8 + warp;
-  uint4 w[U][R];
-  auto fetch = [&](int n0, int k0) {
+// Then the tokens' scales, and their codes of the chunks k0 .. k0 + n - 1 as rows 0 .. M - 1 of the
+// operand (rows from M on hold whatever was there: their columns of the product are not read).
+template <typename T>
+__device__ __forceinline__ void ss_quantize(const SsArgs& a, uint8_t* operand, float* scale, const uint32_t* most,
+                                            int k0, int n, int tid) {
+  auto of = [&](int t) { return SqScale(max(max(most[4 * t], most[4 * t + 1]), max(most[4 * t + 2], most[4 * t + 3]))); };
+  for (int i = tid; i < 16 * n; i += 128) {  // run i: 8 codes, half a 16-byte unit of the swizzled row
+    const int c = i >> 4, u = (i & 15) >> 1, k = (k0 + c) * kSgChunk + 8 * (i & 15);
 #pragma unroll
-    for (int u = 0; u < U; u++)
-#pragma unroll
-      for (int r = 0; r < R; r++) {
-        const int k = k0 + 512 * u + 16 * lane;
-        w[u][r] = k < a.K && n0 + r < a.N ? sv_codes(a.w + (long long)(n0 + r) * a.ldw, k, a.K) : make_uint4(0u, 0u, 0u, 0u);
+    for (int t = 0; t < kSsFusedTokens; t++) {
+      if (t < a.M) {
+        const SqScale q = of(t);
+        SqRun<T> h;
+        if (q.some() && k < a.K) h.load(static_cast<const T*>(a.x.x) + t * a.x.ldx, k, a.K, a.x.vec_x != 0);
+        else h.zero();
+        sq_store8(reinterpret_cast<int8_t*>(operand) + c * kSsFusedRow + t * kSgChunk + ((u ^ t) << 4) + 8 * (i & 1), 0, 8, h,
+                  q.s);
       }
+    }
+  }
+  if (tid < a.M) scale[tid] = of(tid).scale();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_constant__ SsArgs a) {
+  constexpr bool FUSED = !std::is_same<T, int8_t>::value;
+  extern __shared__ __align__(128) uint8_t ss_smem[];
+  const uint32_t pad = (1024u - (smem_u32(ss_smem) & 1023u)) & 1023u;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = a.stages, P = a.splits;
+  const uint32_t rank = P > 1 ? cluster_rank() : 0u;
+  const int n0 = int(blockIdx.x) / P * kSgRows, kc = (a.K + kSgChunk - 1) / kSgChunk;
+  const int k0 = int(rank) * kc / P, nk = (int(rank) + 1) * kc / P - k0;  // this CTA's chunks
+  uint8_t* stages = ss_smem + pad;
+  uint8_t* operand = stages + size_t(S) * a.stage_bytes;
+  // the sums of the tokens this CTA finishes, [sender][token][128 channels]
+  uint32_t* sums = reinterpret_cast<uint32_t*>(operand + (FUSED ? uint32_t((kc + P - 1) / P) * kSsFusedRow : 0u));
+  uint8_t* region = reinterpret_cast<uint8_t*>(sums) + (P > 1 ? size_t(P) * a.slice * kSgRows * 4 : 0);
+  uint64_t* full = reinterpret_cast<uint64_t*>(region);
+  uint64_t* empty = full + kSgMaxStages;
+  uint64_t* acc_full = empty + kSgMaxStages;
+  uint64_t* tok_full = acc_full + 1;
+  uint64_t* sums_full = tok_full + 1;
+  // words: [0] tensor-memory address, [1] a role stopped, [2] copies issued
+  uint32_t* words = reinterpret_cast<uint32_t*>(region + 224);
+  float* scale = reinterpret_cast<float*>(region + 256);
+  uint32_t* most = reinterpret_cast<uint32_t*>(region + 512);
+  uint32_t* stop = &words[1];
+  const uint32_t bytes = kSgWBytes + (FUSED ? 0u : uint32_t(a.nn) * kSgChunk);
+  const bool copier = warp == kSgCopyWarp && lane == 0;
+  auto copy_weights = [&](int j, int st) {
+    mbar_expect_tx(&full[st], bytes);
+    sg_copy_3d<1>(stages + size_t(st) * a.stage_bytes, &a.wmap, (k0 + j) * kSgChunk, n0, 0, smem_u32(&full[st]));
   };
-  fetch(min(g, groups - 1) * R, 0);
-  sv_stage<T, TOK>(a, sv_codes_smem, scale, most, Kp);
-  for (; g < groups; g += step) {
-    const int n0 = g * R;
-    int acc[R][TOK] = {};
-    for (int k0 = 0; k0 < Kp; k0 += 512 * U) {
-      uint4 v[U][R];
-#pragma unroll
-      for (int u = 0; u < U; u++)
-#pragma unroll
-        for (int r = 0; r < R; r++) v[u][r] = w[u][r];
-      if (k0 + 512 * U < Kp) fetch(n0, k0 + 512 * U);
-      else if (g + step < groups) fetch((g + step) * R, 0);
-#pragma unroll
-      for (int u = 0; u < U; u++) {
-        if (k0 + 512 * u < Kp) {
-#pragma unroll
-          for (int t = 0; t < TOK; t++) {
-            const int4 x = *reinterpret_cast<const int4*>(sv_codes_smem + t * Kp + k0 + 512 * u + 16 * lane);
-#pragma unroll
-            for (int r = 0; r < R; r++) {
-              acc[r][t] = __dp4a(int(v[u][r].x), x.x, acc[r][t]);
-              acc[r][t] = __dp4a(int(v[u][r].y), x.y, acc[r][t]);
-              acc[r][t] = __dp4a(int(v[u][r].z), x.z, acc[r][t]);
-              acc[r][t] = __dp4a(int(v[u][r].w), x.w, acc[r][t]);
-            }
-          }
+  auto copy_tokens = [&](int j, int st) {
+    if constexpr (!FUSED)
+      sg_copy_2d<1>(stages + size_t(st) * a.stage_bytes + kSgWBytes, &a.qmap, (k0 + j) * kSgChunk, 0, smem_u32(&full[st]));
+  };
+
+  const int first = min(S, nk);
+  if (copier) {  // before any other setup: the weights' first copies
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&a.wmap)) : "memory");
+    for (int i = 0; i < S; i++) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(tok_full, 4);
+    mbar_init(sums_full, 1);
+    fence_mbar_init();
+    if (P > 1) mbar_expect_tx(sums_full, uint32_t(P * max(0, min(a.slice, a.M - int(rank) * a.slice))) * kSgRows * 4u);
+    if (!a.ahead) pdl_wait();
+    for (int j = 0; j < first; j++) copy_weights(j, j);
+  }
+  if (tid == 0)
+    for (int i = 1; i < 8; i++) words[i] = 0;
+  if (warp == kSgMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(words)), "r"(a.cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  if (FUSED && warp < 4) {  // x is read before the weights fill the memory's queues
+    pdl_wait();
+    ss_maxima<T>(a, most, tid);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // Arrived once this CTA's barriers are set up (fence_mbar_init orders that for the cluster), waited for
+  // before a peer is written to. Relaxed: a release here waits for the copies in flight, 2 us when the
+  // memory is busy with weights.
+  if (P > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
+  const uint32_t tmem = words[0];
+  pdl_wait();
+  pdl_trigger();  // only now: what follows may count on everything before this kernel being complete
+
+  if (warp == kSgCopyWarp) {
+    if (lane == 0) {
+      bool ok = true;
+      int j = 0, st = 0;
+      uint32_t ph = 1;
+      for (; j < nk; j++) {
+        if (j >= first) {
+          if (!(ok = tc_wait(&empty[st], ph, stop))) break;
+          copy_weights(j, st);
         }
+        copy_tokens(j, st);
+        if (++st == S) { st = 0; ph ^= 1; }
+      }
+      if (!ok) *reinterpret_cast<volatile uint32_t*>(stop) = 1u;
+      words[2] = uint32_t(j);
+      for (int i = 0; i < first && ok; i++) {  // every stage's MMAs have arrived before this CTA may end
+        if (--st < 0) { st = S - 1; ph ^= 1; }
+        ok = tc_wait(&empty[st], ph ^ 1u, stop);
       }
     }
-    int mine = 0;  // lane R t + r: token t, channel n0 + r
+  } else if (warp == kSgMmaWarp) {
+    if (lane == 0) {
+      const uint32_t idesc = sg_idesc(a.nn, kSgRows);
+      bool ok = !FUSED || tc_wait(tok_full, 0, stop);
+      int st = 0;
+      uint32_t ph = 0;
+      for (int j = 0; j < nk && ok; j++) {
+        if (!(ok = tc_wait(&full[st], ph, stop))) break;
+        tc_fence_after();
+        const uint32_t wa = smem_u32(stages + size_t(st) * a.stage_bytes);
+        const uint64_t da = sg_desc(wa), db = sg_desc(FUSED ? smem_u32(operand) + uint32_t(j) * kSsFusedRow : wa + kSgWBytes);
 #pragma unroll
-    for (int t = 0; t < TOK; t++)
-#pragma unroll
-      for (int r = 0; r < R; r++) {
-        const int sum = __reduce_add_sync(0xffffffffu, acc[r][t]);
-        if (lane == R * t + r) mine = sum;
+        for (int i = 0; i < kSgChunk / 32; i++) sg_mma<1>(tmem, da + 2 * i, db + 2 * i, idesc, j > 0 || i > 0);
+        tc_commit(&empty[st]);
+        if (++st == S) { st = 0; ph ^= 1; }
       }
-    const int t = lane / R, n = n0 + lane % R;
-    if (t < a.M && t < TOK && n < a.N) {
-      const float s = __fmul_rn(scale[t], __ldg(a.w_scale + n)), v = float(mine);
-      const float y = a.bias ? __fmaf_rn(v, s, __ldg(a.bias + n)) : __fmul_rn(v, s);
-      const long long at = t * a.ldy + n;
-      if (a.y_type == BQ_TYPE_F32) sg_put(static_cast<float*>(a.y) + at, y);
-      else if (a.y_type == BQ_TYPE_BF16) sg_put(static_cast<__nv_bfloat16*>(a.y) + at, y);
-      else sg_put(static_cast<__half*>(a.y) + at, y);
+      if (ok) tc_commit(acc_full);
+      else *reinterpret_cast<volatile uint32_t*>(stop) = 1u;
     }
+  } else {
+    const int n = n0 + tid;  // this thread's channel
+    const bool live = n < a.N;
+    const float sw = live ? __ldg(a.w_scale + n) : 0.f, b = a.bias && live ? __ldg(a.bias + n) : 0.f;
+    if constexpr (FUSED) {
+      ss_quantize<T>(a, operand, scale, most, k0, nk, tid);
+      fence_proxy_async();  // the codes are read by the MMA
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tok_full);
+    } else if (tid < a.M) {
+      scale[tid] = __ldg(a.scale + tid);
+    }
+    asm volatile("bar.sync 1, 128;\n" ::: "memory");  // the scales are written
+    bool ok = __all_sync(0xffffffffu, tc_wait(acc_full, 0, stop));
+    tc_fence_after();
+    const uint32_t acc = tmem + (uint32_t(32 * warp) << 16);
+    if (P == 1) {
+      for (int c = 0; ok && c < a.M; c += 8) {
+        uint32_t v[8];
+        ss_ld8(acc + uint32_t(c), v);
+        if (live) ss_out(a, c, min(c + 8, a.M), n, scale, sw, b, [&](int m) {
+            uint32_t o = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i++) o = m - c == i ? v[i] : o;
+            return o;
+          });
+      }
+    } else {
+      // this CTA's sums as [token][channel], over the stages (whose MMAs are done), then each CTA its
+      // slice of the tokens, to [this CTA][token of the slice][channel] there
+      uint32_t* mine = reinterpret_cast<uint32_t*>(stages);
+      for (int c = 0; ok && c < a.M; c += 8) {
+        uint32_t v[8];
+        ss_ld8(acc + uint32_t(c), v);
+#pragma unroll
+        for (int i = 0; i < 8; i++) mine[(c + i) * kSgRows + tid] = v[i];
+      }
+      fence_proxy_async();
+      asm volatile("bar.sync 1, 128;\n" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok && tid < P && tid * a.slice < a.M)
+        dsmem_copy(dsmem_map(smem_u32(sums + int(rank) * a.slice * kSgRows), uint32_t(tid)), smem_u32(mine + tid * a.slice * kSgRows),
+                   uint32_t(min(a.slice, a.M - tid * a.slice)) * kSgRows * 4u, dsmem_map(smem_u32(sums_full), uint32_t(tid)));
+      const int m0 = int(rank) * a.slice, m1 = min(m0 + a.slice, a.M);
+      if (m0 < m1) {
+        ok = __all_sync(0xffffffffu, ok && tc_wait(sums_full, 0, stop));
+        if (ok && live) ss_out(a, m0, m1, n, scale, sw, b, [&](int m) {
+            const uint32_t* v = sums + (m - m0) * kSgRows + tid;
+            uint32_t o = 0;
+#pragma unroll
+            for (int p = 0; p < kSsMaxSplit; p++) o += p < P ? v[p * a.slice * kSgRows] : 0u;
+            return o;
+          });
+      }
+    }
+    if (!ok && lane == 0) *reinterpret_cast<volatile uint32_t*>(stop) = 1u;
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSgMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(a.cols) : "memory");
+  }
+  if (words[1]) {  // a role gave up: copies it had issued are given time to land, and peers to be done with it
+    if (tid == 0) {
+      const int issued = max(int(words[2]), first);
+      for (int j = max(0, issued - S); j < issued; j++) mbar_wait_bounded(&full[j % S], uint32_t((j / S) & 1));
+      for (int j = 0; j < 1000; j++) __nanosleep(1000);
+    }
+    __syncthreads();
+  }
+  // no CTA leaves while its sums are being copied out of its shared memory, or a peer's into it
+  if (P > 1) {
+    __syncwarp();
+    if (warp >= 4) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
   }
 }
 

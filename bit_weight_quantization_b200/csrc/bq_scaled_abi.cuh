@@ -181,56 +181,102 @@ inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long ti
   return BQ_OK;
 }
 
-// One to kSvMaxTokens tokens whose codes fit in shared memory take the pass over the weights.
-inline bool scaled_few_tokens(int M, int K) {
-  const int tok = pow2ceil(M);
-  return M <= kSvMaxTokens && tok * ((K + 511) / 512 * 512) <= kSvMaxCodes;
-}
+// The split kernel for M tokens (M <= kSsMaxTokens): clusters of `splits` CTAs per 128 channels, as
+// many as minimise waves x (chunks a CTA + kSsFixed), a wave being as many clusters as the device holds
+// at once; kSsFixed is what a CTA costs beside its chunks (first copies, sums, output), in chunks.
+constexpr int kSsFixed = 8;
+constexpr uint32_t kSsSmemTwo = 113 * 1024;  // shared memory that leaves room for a second CTA
 
-template <typename T, int TOK, int R>
-inline bq_status launch_scaled_gemv_r(const SvArgs& a, cudaStream_t s) {
-  auto k = k_scaled_gemv<T, TOK, R>;
+template <typename T>
+inline bq_status launch_scaled_split(SsArgs a, cudaStream_t s) {
+  constexpr bool FUSED = !std::is_same<T, int8_t>::value;
+  auto k = k_scaled_split<T>;
+  const int tiles = (a.N + kSgRows - 1) / kSgRows, kc = (a.K + kSgChunk - 1) / kSgChunk;
+  a.nn = (a.M + 15) / 16 * 16;
+  a.cols = 32;
+  while (a.cols < a.nn) a.cols *= 2;
+  a.stage_bytes = int(kSgWBytes) + (FUSED ? 0 : a.nn * kSgChunk);
+  auto shape = [&](int p) {  // stages and shared memory of p splits
+    const int chunks = (kc + p - 1) / p;
+    a.splits = p;
+    a.slice = (a.M + p - 1) / p;
+    const uint32_t fixed = 1024 + kSsRegion + (FUSED ? uint32_t(chunks) * kSsFusedRow : 0u) +
+                           (p > 1 ? uint32_t(p * a.slice) * kSgRows * 4u : 0u);
+    const uint32_t room = fixed + 3u * uint32_t(a.stage_bytes) <= kSsSmemTwo ? kSsSmemTwo : kTcSmemMax;
+    // the stages also hold the CTA's sums, 512 bytes a token, before they are sent: two at least beyond 32 tokens
+    const int most = std::max(a.M > 32 ? 2 : 1, std::min(kSgMaxStages, chunks));
+    a.stages = fixed >= room ? 0 : std::min(most, int((room - fixed) / uint32_t(a.stage_bytes)));
+    return fixed + uint32_t(a.stages * a.stage_bytes);
+  };
   static std::mutex mu;
   static unsigned long long set_ctx = 0;
-  const unsigned smem = unsigned(TOK * ((a.K + 511) / 512 * 512));
-  if (smem > 40 * 1024) {
+  static int max_clusters[kSsMaxSplit + 1];  // at the largest shared memory of two CTAs an SM
+  int best = 1;
+  {
     const unsigned long long ctx = current_context_id();
     std::lock_guard<std::mutex> lock(mu);
     if (ctx == 0 || ctx != set_ctx) {
-      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSvMaxCodes) != cudaSuccess) {
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kTcSmemMax)) != cudaSuccess) {
         (void)cudaGetLastError();
         return BQ_ERR_CUDA;
       }
+      for (int c = 1; c <= kSsMaxSplit; c++) {
+        cudaLaunchConfig_t q = {};
+        q.gridDim = dim3(unsigned(c));
+        q.blockDim = dim3(kSgThreads);
+        q.dynamicSmemBytes = kSsSmemTwo;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = unsigned(c);
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        q.attrs = at;
+        q.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&max_clusters[c], k, &q) != cudaSuccess) {
+          (void)cudaGetLastError();
+          max_clusters[c] = c == 1 ? 2 * sm_count() : 0;  // without the query: no clusters
+        }
+      }
       set_ctx = ctx;
     }
+    long long best_cost = -1;
+    for (int c = 1; c <= kSsMaxSplit && c <= kc; c++) {
+      if (max_clusters[c] <= 0) continue;
+      const long long waves = (tiles + max_clusters[c] - 1) / max_clusters[c], cost = waves * ((kc + c - 1) / c + kSsFixed);
+      if (best_cost < 0 || cost < best_cost) { best = c; best_cost = cost; }
+    }
   }
-  const int blocks = std::min(((a.N + R - 1) / R + 7) / 8, 2 * sm_count());
-  k<<<unsigned(blocks), kSvThreads, smem, s>>>(a);
-  return launch_status();
+  const uint32_t smem = shape(best);
+  if (a.stages < (a.M > 32 ? 2 : 1)) return BQ_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(tiles * best));
+  cfg.blockDim = dim3(kSgThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = unsigned(best);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = best > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, k, a) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return BQ_ERR_CUDA;
+  }
+  return BQ_OK;
 }
 
-template <typename T, int TOK>
-inline bq_status launch_scaled_gemv_t(const SvArgs& a, cudaStream_t s) {
-  // channels a warp: as many as leave every warp of two blocks an SM a group
-  const int warps = 16 * sm_count();
-  if (a.N >= 4 * warps) return launch_scaled_gemv_r<T, TOK, 4>(a, s);
-  if (a.N >= 2 * warps) return launch_scaled_gemv_r<T, TOK, 2>(a, s);
-  return launch_scaled_gemv_r<T, TOK, 1>(a, s);
-}
+// Whether bq_scaled_linear quantizes inside the product: up to kSsFusedTokens tokens, and the codes of
+// one CTA's k-range (of at most 1/8 of K where it is long) within 32 KB
+inline bool scaled_fused(int M, int K) { return M <= kSsFusedTokens && K <= 16384; }
 
-template <typename T>
-inline bq_status launch_scaled_gemv(const SvArgs& a, cudaStream_t s) {
-  if (a.M <= 1) return launch_scaled_gemv_t<T, 1>(a, s);
-  if (a.M <= 2) return launch_scaled_gemv_t<T, 2>(a, s);
-  if (a.M <= 4) return launch_scaled_gemv_t<T, 4>(a, s);
-  return launch_scaled_gemv_t<T, 8>(a, s);
-}
-
-inline SvArgs scaled_gemv_args(const bq_scaled_weights* w, int M, void* y, int y_type, int64_t ldy) {
-  SvArgs a{};
-  a.w = w->codes; a.w_scale = w->scale; a.bias = w->bias; a.y = y; a.ldw = w->ld; a.ldy = ldy;
-  a.M = M; a.N = w->N; a.K = w->K; a.y_type = y_type;
-  return a;
+inline bool split_args(const bq_scaled_weights* w, int M, void* y, int y_type, int64_t ldy, SsArgs* a) {
+  a->w_scale = w->scale; a->bias = w->bias; a->y = y; a->ldy = ldy;
+  a->M = M; a->N = w->N; a->K = w->K; a->y_type = y_type;
+  return encode_codes_map(w->codes, w->ld, w->N, w->K, 1, 0, kSgRows, &a->wmap);
 }
 
 inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_t ldq, const float* scale, int32_t M,
@@ -245,12 +291,13 @@ inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_
   if ((st = check_codes(q, ldq, w->K)) != BQ_OK) return st;
   if ((st = check_values(y, y_type, ldy, w->N)) != BQ_OK) return st;
   if (!scale || !aligned(scale, 4) || (grouped && (!offsets || !aligned(offsets, 4)))) return BQ_ERR_INVALID_ARG;
-  if (!grouped && scaled_few_tokens(M, w->K)) {
-    SvArgs a = scaled_gemv_args(w, M, y, y_type, ldy);
-    a.x.q = const_cast<int8_t*>(q);
-    a.x.ldq = ldq;
-    a.x.scale = const_cast<float*>(scale);
-    return launch_scaled_gemv<int8_t>(a, reinterpret_cast<cudaStream_t>(stream));
+  if (!grouped && M <= kSsMaxTokens) {
+    SsArgs a{};
+    if (!split_args(w, M, y, y_type, ldy, &a) || !encode_codes_map(q, ldq, M, w->K, 0, 0, (M + 15) / 16 * 16, &a.qmap))
+      return BQ_ERR_CUDA;
+    a.scale = scale;
+    a.ahead = after_quantize;
+    return launch_scaled_split<int8_t>(a, reinterpret_cast<cudaStream_t>(stream));
   }
   // 16-bit outputs leave by TMA where their rows start on 16-byte boundaries
   const bool y_tma = y_type != BQ_TYPE_F32 && rows_aligned(y, y_type, ldy);
@@ -336,15 +383,16 @@ bq_status bq_scaled_linear(const bq_scaled_weights* w, const void* x, int32_t x_
   if ((st = check_values(y, y_type, ldy, w->N)) != BQ_OK) return st;
   if (!workspace || !aligned(workspace, 256)) return BQ_ERR_INVALID_ARG;
   if (workspace_bytes < need) return BQ_ERR_SIZE;
-  if (scaled_few_tokens(M, w->K)) {
-    SvArgs a = scaled_gemv_args(w, M, y, y_type, ldy);
+  if (scaled_fused(M, w->K)) {
+    SsArgs a{};
+    if (!split_args(w, M, y, y_type, ldy, &a)) return BQ_ERR_CUDA;
     a.x.x = x;
     a.x.ldx = ldx;
     a.x.vec_x = rows_aligned(x, x_type, ldx);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return x_type == BQ_TYPE_F32    ? launch_scaled_gemv<float>(a, s)
-           : x_type == BQ_TYPE_BF16 ? launch_scaled_gemv<__nv_bfloat16>(a, s)
-                                    : launch_scaled_gemv<__half>(a, s);
+    return x_type == BQ_TYPE_F32    ? launch_scaled_split<float>(a, s)
+           : x_type == BQ_TYPE_BF16 ? launch_scaled_split<__nv_bfloat16>(a, s)
+                                    : launch_scaled_split<__half>(a, s);
   }
   const int64_t ld = scaled_ld(w->K);
   int8_t* q = static_cast<int8_t*>(workspace);
