@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
 // into the operand's swizzled rows, while the weights are on their way: one launch for a decoded token.
 
 constexpr int kSsMaxTokens = 64, kSsFusedTokens = 4;
-constexpr int kSsMaxSplit = 8;
+constexpr int kSsMaxSplit = 8, kSsDirect = 8;
 constexpr uint32_t kSsFusedRow = 16 * kSgChunk;  // a chunk of the fused operand: 16 rows of 128 codes
 // after the stages, the fused operand and the received sums: full[12] (0), empty[12] (96), acc_full
 // (192), tok_full (200), sums_full (208), words[8] (224), token scales [64] (256), maxima [4][4] (512)
@@ -748,6 +748,12 @@ __device__ __forceinline__ void dsmem_copy(uint32_t rdst, uint32_t src, uint32_t
                "r"(src), "r"(bytes), "r"(rbar)
                : "memory");
 }
+// a word to the shared memory of a CTA of the cluster, counted by a barrier there
+__device__ __forceinline__ void dsmem_st_async(uint32_t raddr, uint32_t v, uint32_t rbar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];\n" ::"r"(raddr), "r"(v),
+               "r"(rbar)
+               : "memory");
+}
 // 32 lanes x 8 columns of tensor memory
 __device__ __forceinline__ void ss_ld8(uint32_t taddr, uint32_t (&v)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
@@ -757,50 +763,60 @@ __device__ __forceinline__ void ss_ld8(uint32_t taddr, uint32_t (&v)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 }
 
-// y of this thread's channel for the tokens m0 .. m1 - 1; sum(m) gives their exact sums, eight of them
-// before the first is used
-template <typename Y, typename F>
-__device__ __forceinline__ void ss_out(const SsArgs& a, int m0, int m1, int n, const float* scale, float sw, float b,
-                                       F sum) {
-  Y* y = static_cast<Y*>(a.y) + m0 * a.ldy + n;
-  for (int m = m0; m < m1; m += 8) {
-    int v[8];
+// y of this thread's channel n for up to four tokens from m on, from their exact sums
+template <typename Y>
+__device__ __forceinline__ void ss_put(const SsArgs& a, int m, int count, int n, const float* scale, float sw, float b,
+                                       const uint32_t (&v)[4]) {
+  Y* y = static_cast<Y*>(a.y) + m * a.ldy + n;
 #pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = m + i < m1 ? int(sum(m + i)) : 0;
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-      if (m + i < m1) {
-        const float s = __fmul_rn(scale[m + i], sw), f = float(v[i]);
-        sg_put(y, a.bias ? __fmaf_rn(f, s, b) : __fmul_rn(f, s));
-        y += a.ldy;
-      }
+  for (int i = 0; i < 4; i++) {
+    if (i < count) {
+      const float s = __fmul_rn(scale[m + i], sw), f = float(int(v[i]));
+      sg_put(y, a.bias ? __fmaf_rn(f, s, b) : __fmul_rn(f, s));
+      y += a.ldy;
     }
   }
 }
-template <typename F>
-__device__ __forceinline__ void ss_out(const SsArgs& a, int m0, int m1, int n, const float* scale, float sw, float b,
-                                       F sum) {
-  if (a.y_type == BQ_TYPE_F32) ss_out<float>(a, m0, m1, n, scale, sw, b, sum);
-  else if (a.y_type == BQ_TYPE_BF16) ss_out<__nv_bfloat16>(a, m0, m1, n, scale, sw, b, sum);
-  else ss_out<__half>(a, m0, m1, n, scale, sw, b, sum);
+__device__ __forceinline__ void ss_out(const SsArgs& a, int m, int count, int n, const float* scale, float sw, float b,
+                                       const uint32_t (&v)[4]) {
+  if (a.y_type == BQ_TYPE_F32) ss_put<float>(a, m, count, n, scale, sw, b, v);
+  else if (a.y_type == BQ_TYPE_BF16) ss_put<__nv_bfloat16>(a, m, count, n, scale, sw, b, v);
+  else ss_put<__half>(a, m, count, n, scale, sw, b, v);
 }
 
-// Warps 0-3: every token's largest |x| of this warp's share of the row, to most[4 t + warp].
-template <typename T>
+// 32 lanes x 4 columns of tensor memory
+__device__ __forceinline__ void ss_ld4(uint32_t taddr, uint32_t (&v)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(taddr)
+               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+}
+
+// Warps 0-3: every token's largest |x| of this warp's share of the row, to most[4 t + warp]. The first
+// loads are issued before the copying warp is let go on (barrier 2): behind the weights they would
+// take three times as long.
+template <typename T, int TOK>
 __device__ __forceinline__ void ss_maxima(const SsArgs& a, uint32_t* most, int tid) {
-  uint32_t m[kSsFusedTokens] = {};
-#pragma unroll 2
-  for (int k = 8 * tid; k < a.K; k += 8 * 128) {
-    SqRun<T> h[kSsFusedTokens];
+  constexpr int U = (sizeof(T) == 4 ? 8 : 16) / TOK < 4 ? (sizeof(T) == 4 ? 8 : 16) / TOK : 4;
+  uint32_t m[TOK] = {};
+  for (int k0 = 8 * tid; k0 == 8 * tid || k0 < a.K; k0 += 8 * 128 * U) {
+    SqRun<T> h[U][TOK];
 #pragma unroll
-    for (int t = 0; t < kSsFusedTokens; t++)
-      if (t < a.M) h[t].load(static_cast<const T*>(a.x.x) + t * a.x.ldx, k, a.K, a.x.vec_x != 0);
-      else h[t].zero();
+    for (int u = 0; u < U; u++)
 #pragma unroll
-    for (int t = 0; t < kSsFusedTokens; t++) m[t] = h[t].most(m[t]);
+      for (int t = 0; t < TOK; t++)
+        if (t < a.M && k0 + u * 8 * 128 < a.K)
+          h[u][t].load(static_cast<const T*>(a.x.x) + t * a.x.ldx, k0 + u * 8 * 128, a.K, a.x.vec_x != 0);
+        else h[u][t].zero();
+    if (k0 == 8 * tid) asm volatile("bar.arrive 2, 160;\n" ::: "memory");
+#pragma unroll
+    for (int u = 0; u < U; u++)
+#pragma unroll
+      for (int t = 0; t < TOK; t++) m[t] = h[u][t].most(m[t]);
   }
 #pragma unroll
-  for (int t = 0; t < kSsFusedTokens; t++) {
+  for (int t = 0; t < TOK; t++) {
     m[t] = __reduce_max_sync(0xffffffffu, SqRun<T>::as_float_bits(m[t]));
     if ((tid & 31) == 0) most[4 * t + (tid >> 5)] = m[t];
   }
@@ -808,14 +824,14 @@ __device__ __forceinline__ void ss_maxima(const SsArgs& a, uint32_t* most, int t
 
 // Then the tokens' scales, and their codes of the chunks k0 .. k0 + n - 1 as rows 0 .. M - 1 of the
 // operand (rows from M on hold whatever was there: their columns of the product are not read).
-template <typename T>
+template <typename T, int TOK>
 __device__ __forceinline__ void ss_quantize(const SsArgs& a, uint8_t* operand, float* scale, const uint32_t* most,
                                             int k0, int n, int tid) {
   auto of = [&](int t) { return SqScale(max(max(most[4 * t], most[4 * t + 1]), max(most[4 * t + 2], most[4 * t + 3]))); };
   for (int i = tid; i < 16 * n; i += 128) {  // run i: 8 codes, half a 16-byte unit of the swizzled row
     const int c = i >> 4, u = (i & 15) >> 1, k = (k0 + c) * kSgChunk + 8 * (i & 15);
 #pragma unroll
-    for (int t = 0; t < kSsFusedTokens; t++) {
+    for (int t = 0; t < TOK; t++) {
       if (t < a.M) {
         const SqScale q = of(t);
         SqRun<T> h;
@@ -829,7 +845,7 @@ __device__ __forceinline__ void ss_quantize(const SsArgs& a, uint8_t* operand, f
   if (tid < a.M) scale[tid] = of(tid).scale();
 }
 
-template <typename T>
+template <typename T, int TOK>
 __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_constant__ SsArgs a) {
   constexpr bool FUSED = !std::is_same<T, int8_t>::value;
   extern __shared__ __align__(128) uint8_t ss_smem[];
@@ -876,9 +892,15 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
     mbar_init(sums_full, 1);
     fence_mbar_init();
     if (P > 1) mbar_expect_tx(sums_full, uint32_t(P * max(0, min(a.slice, a.M - int(rank) * a.slice))) * kSgRows * 4u);
-    if (!a.ahead) pdl_wait();
-    for (int j = 0; j < first; j++) copy_weights(j, j);
+    if (!FUSED && !a.ahead) pdl_wait();
   }
+  if (FUSED && warp == kSgCopyWarp) {
+    pdl_wait();
+    __syncwarp();
+    asm volatile("bar.sync 2, 160;\n" ::: "memory");  // the tokens' loads are on their way
+  }
+  if (copier)
+    for (int j = 0; j < first; j++) copy_weights(j, j);
   if (tid == 0)
     for (int i = 1; i < 8; i++) words[i] = 0;
   if (warp == kSgMmaWarp) {
@@ -887,7 +909,7 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
   }
   if (FUSED && warp < 4) {  // x is read before the weights fill the memory's queues
     pdl_wait();
-    ss_maxima<T>(a, most, tid);
+    ss_maxima<T, TOK>(a, most, tid);
   }
   tc_fence_before();
   __syncthreads();
@@ -944,7 +966,7 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
     const bool live = n < a.N;
     const float sw = live ? __ldg(a.w_scale + n) : 0.f, b = a.bias && live ? __ldg(a.bias + n) : 0.f;
     if constexpr (FUSED) {
-      ss_quantize<T>(a, operand, scale, most, k0, nk, tid);
+      ss_quantize<T, TOK>(a, operand, scale, most, k0, nk, tid);
       fence_proxy_async();  // the codes are read by the MMA
       __syncwarp();
       if (lane == 0) mbar_arrive(tok_full);
@@ -956,43 +978,56 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
     tc_fence_after();
     const uint32_t acc = tmem + (uint32_t(32 * warp) << 16);
     if (P == 1) {
-      for (int c = 0; ok && c < a.M; c += 8) {
-        uint32_t v[8];
-        ss_ld8(acc + uint32_t(c), v);
-        if (live) ss_out(a, c, min(c + 8, a.M), n, scale, sw, b, [&](int m) {
-            uint32_t o = 0;
-#pragma unroll
-            for (int i = 0; i < 8; i++) o = m - c == i ? v[i] : o;
-            return o;
-          });
+      for (int c = 0; ok && c < a.M; c += 4) {
+        uint32_t v[4];
+        ss_ld4(acc + uint32_t(c), v);
+        if (live) ss_out(a, c, a.M - c, n, scale, sw, b, v);
       }
     } else {
-      // this CTA's sums as [token][channel], over the stages (whose MMAs are done), then each CTA its
-      // slice of the tokens, to [this CTA][token of the slice][channel] there
-      uint32_t* mine = reinterpret_cast<uint32_t*>(stages);
-      for (int c = 0; ok && c < a.M; c += 8) {
+      // token m's sums to CTA m / slice, at [this CTA][m % slice][channel] there
+      if (a.M <= kSsDirect) {  // few: straight from the registers, and this CTA need not wait for their arrival
         uint32_t v[8];
-        ss_ld8(acc + uint32_t(c), v);
+        ss_ld8(acc, v);
+        __syncwarp();
+        asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 #pragma unroll
-        for (int i = 0; i < 8; i++) mine[(c + i) * kSgRows + tid] = v[i];
+        for (int i = 0; i < kSsDirect; i++) {
+          if (ok && i < a.M) {
+            const uint32_t to = uint32_t(i / a.slice);
+            dsmem_st_async(dsmem_map(smem_u32(sums + (int(rank) * a.slice + i % a.slice) * kSgRows + tid), to), v[i],
+                           dsmem_map(smem_u32(sums_full), to));
+          }
+        }
+      } else {  // over the stages (whose MMAs are done) as [token][channel], then a copy to each CTA
+        uint32_t* mine = reinterpret_cast<uint32_t*>(stages);
+        for (int c = 0; ok && c < a.M; c += 8) {
+          uint32_t v[8];
+          ss_ld8(acc + uint32_t(c), v);
+#pragma unroll
+          for (int i = 0; i < 8; i++) mine[(c + i) * kSgRows + tid] = v[i];
+        }
+        fence_proxy_async();
+        asm volatile("bar.sync 1, 128;\n" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+        if (ok && tid < P && tid * a.slice < a.M)
+          dsmem_copy(dsmem_map(smem_u32(sums + int(rank) * a.slice * kSgRows), uint32_t(tid)), smem_u32(mine + tid * a.slice * kSgRows),
+                     uint32_t(min(a.slice, a.M - tid * a.slice)) * kSgRows * 4u, dsmem_map(smem_u32(sums_full), uint32_t(tid)));
+        __syncwarp();
       }
-      fence_proxy_async();
-      asm volatile("bar.sync 1, 128;\n" ::: "memory");
-      asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok && tid < P && tid * a.slice < a.M)
-        dsmem_copy(dsmem_map(smem_u32(sums + int(rank) * a.slice * kSgRows), uint32_t(tid)), smem_u32(mine + tid * a.slice * kSgRows),
-                   uint32_t(min(a.slice, a.M - tid * a.slice)) * kSgRows * 4u, dsmem_map(smem_u32(sums_full), uint32_t(tid)));
       const int m0 = int(rank) * a.slice, m1 = min(m0 + a.slice, a.M);
       if (m0 < m1) {
         ok = __all_sync(0xffffffffu, ok && tc_wait(sums_full, 0, stop));
-        if (ok && live) ss_out(a, m0, m1, n, scale, sw, b, [&](int m) {
-            const uint32_t* v = sums + (m - m0) * kSgRows + tid;
-            uint32_t o = 0;
+        for (int m = m0; ok && live && m < m1; m += 4) {
+          uint32_t v[4];
 #pragma unroll
-            for (int p = 0; p < kSsMaxSplit; p++) o += p < P ? v[p * a.slice * kSgRows] : 0u;
-            return o;
-          });
+          for (int i = 0; i < 4; i++) {
+            v[i] = 0;
+#pragma unroll
+            for (int q = 0; q < kSsMaxSplit; q++)
+              if (q < P && m + i < m1) v[i] += sums[(q * a.slice + m + i - m0) * kSgRows + tid];
+          }
+          ss_out(a, m, m1 - m, n, scale, sw, b, v);
+        }
       }
     }
     if (!ok && lane == 0) *reinterpret_cast<volatile uint32_t*>(stop) = 1u;
@@ -1012,8 +1047,9 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
     }
     __syncthreads();
   }
-  // no CTA leaves while its sums are being copied out of its shared memory, or a peer's into it
-  if (P > 1) {
+  // no CTA leaves while its sums are being copied out of its shared memory; nor, if it did not get all that
+  // it waited for, while a peer may still write to it (threads that have left count as arrived)
+  if (P > 1 && (a.M > kSsDirect || words[1])) {
     __syncwarp();
     if (warp >= 4) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");

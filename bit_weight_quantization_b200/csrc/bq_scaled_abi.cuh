@@ -181,37 +181,31 @@ inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long ti
   return BQ_OK;
 }
 
-// The split kernel for M tokens (M <= kSsMaxTokens): clusters of `splits` CTAs per 128 channels, as
-// many as minimise waves x (chunks a CTA + kSsFixed), a wave being as many clusters as the device holds
-// at once; kSsFixed is what a CTA costs beside its chunks (first copies, sums, output), in chunks.
-constexpr int kSsFixed = 8;
-constexpr uint32_t kSsSmemTwo = 113 * 1024;  // shared memory that leaves room for a second CTA
+// The split kernel for M tokens (M <= kSsMaxTokens): clusters of `splits` CTAs per 128 channels, each
+// CTA within half of an SM's shared memory. Two then run on an SM, or one beside the next launch's first
+// (with the whole of it, one token of 4096 x 4096 took 9.7 us among others instead of 6.6).
+constexpr uint32_t kSsSmem = 113 * 1024;
 
-template <typename T>
+// What p splits are expected to take, in ns, with `active` CTAs of `stages` stages at work: a chunk of 16 KB
+// of weights per CTA and latency / stages (1.5 us, 2.3 where two CTAs share an SM), but no faster than
+// 6.3 TB/s for all; 3 us for launch, first copies and output; 0.25 us a CTA of the cluster and 20 ns a
+// token where there are sums to exchange. (Measured, in us: one token, 4096 x 4096: 6.6 in four, 7.2 in
+// eight; 13824 x 5120: 15.1 whole, 14.4 in two; 64 tokens: 4096 x 4096 16.5 whole, 9.8 in four;
+// 13824 x 5120 18.2 whole, 20.1 in two.)
+inline double scaled_split_ns(int p, int chunks, int stages, long long active, long long waves, int M) {
+  const double latency = active > sm_count() ? 2300.0 : 1500.0;
+  const double chunk = std::max(latency / stages, double(active) * kSgWBytes / 6300.0);
+  return double(waves) * (chunks * chunk + 3000.0) + 250.0 * p + (p > 1 ? 20.0 * M : 0.0);
+}
+
+template <typename T, int TOK>
 inline bq_status launch_scaled_split(SsArgs a, cudaStream_t s) {
   constexpr bool FUSED = !std::is_same<T, int8_t>::value;
-  auto k = k_scaled_split<T>;
-  const int tiles = (a.N + kSgRows - 1) / kSgRows, kc = (a.K + kSgChunk - 1) / kSgChunk;
-  a.nn = (a.M + 15) / 16 * 16;
-  a.cols = 32;
-  while (a.cols < a.nn) a.cols *= 2;
-  a.stage_bytes = int(kSgWBytes) + (FUSED ? 0 : a.nn * kSgChunk);
-  auto shape = [&](int p) {  // stages and shared memory of p splits
-    const int chunks = (kc + p - 1) / p;
-    a.splits = p;
-    a.slice = (a.M + p - 1) / p;
-    const uint32_t fixed = 1024 + kSsRegion + (FUSED ? uint32_t(chunks) * kSsFusedRow : 0u) +
-                           (p > 1 ? uint32_t(p * a.slice) * kSgRows * 4u : 0u);
-    const uint32_t room = fixed + 3u * uint32_t(a.stage_bytes) <= kSsSmemTwo ? kSsSmemTwo : kTcSmemMax;
-    // the stages also hold the CTA's sums, 512 bytes a token, before they are sent: two at least beyond 32 tokens
-    const int most = std::max(a.M > 32 ? 2 : 1, std::min(kSgMaxStages, chunks));
-    a.stages = fixed >= room ? 0 : std::min(most, int((room - fixed) / uint32_t(a.stage_bytes)));
-    return fixed + uint32_t(a.stages * a.stage_bytes);
-  };
+  auto k = k_scaled_split<T, TOK>;
   static std::mutex mu;
   static unsigned long long set_ctx = 0;
-  static int max_clusters[kSsMaxSplit + 1];  // at the largest shared memory of two CTAs an SM
-  int best = 1;
+  static int max_clusters[kSsMaxSplit + 1];  // of one CTA an SM: the query allows a kernel with tensor memory no second
+  int clusters[kSsMaxSplit + 1];
   {
     const unsigned long long ctx = current_context_id();
     std::lock_guard<std::mutex> lock(mu);
@@ -224,7 +218,7 @@ inline bq_status launch_scaled_split(SsArgs a, cudaStream_t s) {
         cudaLaunchConfig_t q = {};
         q.gridDim = dim3(unsigned(c));
         q.blockDim = dim3(kSgThreads);
-        q.dynamicSmemBytes = kSsSmemTwo;
+        q.dynamicSmemBytes = kTcSmemMax;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeClusterDimension;
         at[0].val.clusterDim.x = unsigned(c);
@@ -234,22 +228,45 @@ inline bq_status launch_scaled_split(SsArgs a, cudaStream_t s) {
         q.numAttrs = 1;
         if (cudaOccupancyMaxActiveClusters(&max_clusters[c], k, &q) != cudaSuccess) {
           (void)cudaGetLastError();
-          max_clusters[c] = c == 1 ? 2 * sm_count() : 0;  // without the query: no clusters
+          max_clusters[c] = c == 1 ? sm_count() : 0;  // without the query: no clusters
         }
       }
       set_ctx = ctx;
     }
-    long long best_cost = -1;
-    for (int c = 1; c <= kSsMaxSplit && c <= kc; c++) {
-      if (max_clusters[c] <= 0) continue;
-      const long long waves = (tiles + max_clusters[c] - 1) / max_clusters[c], cost = waves * ((kc + c - 1) / c + kSsFixed);
-      if (best_cost < 0 || cost < best_cost) { best = c; best_cost = cost; }
+    std::memcpy(clusters, max_clusters, sizeof(clusters));
+  }
+  const int tiles = (a.N + kSgRows - 1) / kSgRows, kc = (a.K + kSgChunk - 1) / kSgChunk;
+  a.nn = (a.M + 15) / 16 * 16;
+  a.cols = 32;
+  while (a.cols < a.nn) a.cols *= 2;
+  a.stage_bytes = int(kSgWBytes) + (FUSED ? 0 : a.nn * kSgChunk);
+  // the stages also hold the CTA's sums, 512 bytes a token, before they are copied: two at least beyond 32 tokens
+  const int least = a.M > 32 ? 2 : 1;
+  double best = -1;
+  uint32_t smem = 0;
+  SsArgs run = a;
+  for (int p = 1; p <= kSsMaxSplit && p <= kc; p++) {
+    if (clusters[p] <= 0) continue;
+    const int slots = 2 * clusters[p], chunks = (kc + p - 1) / p;
+    SsArgs t = a;
+    t.splits = p;
+    t.slice = (a.M + p - 1) / p;
+    const uint32_t fixed = 1024 + kSsRegion + (FUSED ? uint32_t(chunks) * kSsFusedRow : 0u) +
+                           (p > 1 ? uint32_t(p * t.slice) * kSgRows * 4u : 0u);
+    const uint32_t room = fixed + uint32_t(2 * t.stage_bytes) > kSsSmem ? kTcSmemMax : kSsSmem;
+    if (fixed + uint32_t(least * t.stage_bytes) > room) continue;
+    t.stages = std::min(std::max(least, std::min(kSgMaxStages, chunks)), int((room - fixed) / uint32_t(t.stage_bytes)));
+    const long long waves = (tiles + slots - 1) / slots, active = (long long)std::min(tiles, slots) * p;
+    const double ns = scaled_split_ns(p, chunks, t.stages, active, waves, a.M) + (room > kSsSmem ? 3000.0 : 0.0);
+    if (best < 0 || ns < best) {
+      best = ns;
+      run = t;
+      smem = fixed + uint32_t(t.stages * t.stage_bytes);
     }
   }
-  const uint32_t smem = shape(best);
-  if (a.stages < (a.M > 32 ? 2 : 1)) return BQ_ERR_UNSUPPORTED;
+  if (best < 0) return BQ_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(tiles * best));
+  cfg.gridDim = dim3(unsigned(tiles * run.splits));
   cfg.blockDim = dim3(kSgThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -257,16 +274,22 @@ inline bq_status launch_scaled_split(SsArgs a, cudaStream_t s) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = unsigned(best);
+  at[1].val.clusterDim.x = unsigned(run.splits);
   at[1].val.clusterDim.y = 1;
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = best > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, k, a) != cudaSuccess) {
+  cfg.numAttrs = run.splits > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, k, run) != cudaSuccess) {
     (void)cudaGetLastError();
     return BQ_ERR_CUDA;
   }
   return BQ_OK;
+}
+
+template <typename T>
+inline bq_status launch_scaled_fused(const SsArgs& a, cudaStream_t s) {
+  static_assert(kSsFusedTokens == 4, "instantiations");
+  return a.M == 1 ? launch_scaled_split<T, 1>(a, s) : a.M == 2 ? launch_scaled_split<T, 2>(a, s) : launch_scaled_split<T, 4>(a, s);
 }
 
 // Whether bq_scaled_linear quantizes inside the product: up to kSsFusedTokens tokens, and the codes of
@@ -297,7 +320,7 @@ inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_
       return BQ_ERR_CUDA;
     a.scale = scale;
     a.ahead = after_quantize;
-    return launch_scaled_split<int8_t>(a, reinterpret_cast<cudaStream_t>(stream));
+    return launch_scaled_split<int8_t, 1>(a, reinterpret_cast<cudaStream_t>(stream));
   }
   // 16-bit outputs leave by TMA where their rows start on 16-byte boundaries
   const bool y_tma = y_type != BQ_TYPE_F32 && rows_aligned(y, y_type, ldy);
@@ -390,9 +413,9 @@ bq_status bq_scaled_linear(const bq_scaled_weights* w, const void* x, int32_t x_
     a.x.ldx = ldx;
     a.x.vec_x = rows_aligned(x, x_type, ldx);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return x_type == BQ_TYPE_F32    ? launch_scaled_split<float>(a, s)
-           : x_type == BQ_TYPE_BF16 ? launch_scaled_split<__nv_bfloat16>(a, s)
-                                    : launch_scaled_split<__half>(a, s);
+    return x_type == BQ_TYPE_F32    ? launch_scaled_fused<float>(a, s)
+           : x_type == BQ_TYPE_BF16 ? launch_scaled_fused<__nv_bfloat16>(a, s)
+                                    : launch_scaled_fused<__half>(a, s);
   }
   const int64_t ld = scaled_ld(w->K);
   int8_t* q = static_cast<int8_t*>(workspace);
