@@ -339,6 +339,18 @@ __device__ __forceinline__ void sg_copy_3d(void* dst, const TcTensorMap* map, in
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+// One lane of a converged warp. The copying and the MMA warp run their loops with all lanes and let one
+// issue: addresses and descriptors then stay in uniform registers. From a branch that only lane 0 takes, an
+// MMA took 76 cycles to issue and a chunk of four 594, whatever its tokens.
+__device__ __forceinline__ bool sg_elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// tc_wait of a converged warp
+__device__ __forceinline__ bool sg_wait(uint64_t* bar, uint32_t parity, const uint32_t* stop) {
+  return __all_sync(0xffffffffu, tc_wait(bar, parity, stop));
+}
 __device__ __forceinline__ void sg_arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
@@ -538,7 +550,7 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
   uint32_t* words = reinterpret_cast<uint32_t*>(region + 224);
   float* tok = reinterpret_cast<float*>(region + 256);
   int* first = reinterpret_cast<int*>(region + kSgRegion);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = a.stages;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), S = a.stages;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int kc = (a.K + kSgChunk - 1) / kSgChunk;
   const int unit = blockIdx.x / CG, units = gridDim.x / CG;
@@ -574,7 +586,7 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
   __syncthreads();
   if constexpr (CG == 2) cluster_sync_all();  // the peer's barriers and tensor memory are ready
   tc_fence_after();
-  const uint32_t tmem = words[0];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, words[0], 0);
   SgWalk walk(a, first, kSgRows * CG);
   SgTile t;
   // this CTA's failure is told to its peer, whose waits then end too
@@ -585,73 +597,82 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
   };
 
   if (warp == kSgCopyWarp) {
-    if (lane == 0) {
-      int st = 0, issued = 0, ahead = 0;
-      uint32_t ph = 1;
-      bool ok = true;
-      // tokens of a tile's MMA, and this CTA's part of them
-      auto part_of = [&](const SgTile& o) { return (o.n + 16 * CG - 1) / (16 * CG) * 16; };
-      auto bar_of = [&](int i) { return CG == 2 ? dsmem_map(smem_u32(&full[i]), 0u) : smem_u32(&full[i]); };
-      auto copy_weights = [&](int i, int k) {
-        if (rank == 0) mbar_expect_tx(&full[i], CG * (kSgWBytes + uint32_t(part_of(t)) * kSgChunk));
-        sg_copy_3d<CG>(stages + size_t(i) * a.stage_bytes, &a.wmap, k * kSgChunk, t.n0 + int(rank) * kSgRows,
-                       min(t.e, a.w_experts - 1), bar_of(i));
-      };
-      // the weights are constant: the first stages' are fetched before the wait for the kernel that
-      // makes the tokens' codes (a whole product's tiles do not hang on device data)
-      if (!a.offsets && walk.at(unit, &t))
-        for (; ahead < min(S, kc); ahead++) copy_weights(ahead, ahead);
-      pdl_wait();
-      for (int u = unit; ok && walk.at(u, &t); u += units) {
-        const int part = part_of(t), m = t.m0 + int(rank) * part;
-        for (int k = 0; k < kc; k++) {
-          if (issued >= ahead) {
-            if (!(ok = tc_wait(&empty[st], ph, stop))) break;
-            copy_weights(st, k);
-          }
+    const bool lead = sg_elect();
+    int st = 0, issued = 0, ahead = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    // tokens of a tile's MMA, and this CTA's part of them
+    auto part_of = [&](const SgTile& o) { return (o.n + 16 * CG - 1) / (16 * CG) * 16; };
+    auto bar_of = [&](int i) { return CG == 2 ? dsmem_map(smem_u32(&full[i]), 0u) : smem_u32(&full[i]); };
+    auto copy_weights = [&](int i, int k) {
+      if (rank == 0) mbar_expect_tx(&full[i], CG * (kSgWBytes + uint32_t(part_of(t)) * kSgChunk));
+      sg_copy_3d<CG>(stages + size_t(i) * a.stage_bytes, &a.wmap, k * kSgChunk, t.n0 + int(rank) * kSgRows,
+                     min(t.e, a.w_experts - 1), bar_of(i));
+    };
+    // the weights are constant: the first stages' are fetched before the wait for the kernel that
+    // makes the tokens' codes (a whole product's tiles do not hang on device data)
+    if (!a.offsets && walk.at(unit, &t)) {
+      ahead = min(S, kc);
+      if (lead)
+        for (int k = 0; k < ahead; k++) copy_weights(k, k);
+    }
+    pdl_wait();
+    for (int u = unit; ok && walk.at(u, &t); u += units) {
+      const int part = part_of(t), m = t.m0 + int(rank) * part;
+      for (int k = 0; k < kc; k++) {
+        const bool fresh = issued >= ahead;
+        if (fresh && !(ok = sg_wait(&empty[st], ph, stop))) break;
+        if (lead) {
+          if (fresh) copy_weights(st, k);
           uint8_t* dst = stages + size_t(st) * a.stage_bytes + kSgWBytes;
           if (part * CG == a.bn) {
             sg_copy_2d<CG>(dst, &a.qmap, k * kSgChunk, m, bar_of(st));
           } else {
             for (int i = 0; i < part; i += 16) sg_copy_2d<CG>(dst + i * kSgChunk, &a.qmap16, k * kSgChunk, m + i, bar_of(st));
           }
-          issued++;
-          if (++st == S) { st = 0; ph ^= 1; }
         }
-      }
-      if (!ok) give_up();
-      words[3] = uint32_t(issued);
-      // every stage's last MMAs have read it (and their arrivals have landed) before this CTA may end
-      for (int i = 0; i < min(S, issued) && ok; i++) {
-        if (--st < 0) { st = S - 1; ph ^= 1; }
-        ok = tc_wait(&empty[st], ph ^ 1u, stop);
+        __syncwarp();
+        issued++;
+        if (++st == S) { st = 0; ph ^= 1; }
       }
     }
+    if (lead) {
+      if (!ok) give_up();
+      words[3] = uint32_t(issued);
+    }
+    // every stage's last MMAs have read it (and their arrivals have landed) before this CTA may end
+    for (int i = 0; i < min(S, issued) && ok; i++) {
+      if (--st < 0) { st = S - 1; ph ^= 1; }
+      ok = sg_wait(&empty[st], ph ^ 1u, stop);
+    }
   } else if (warp == kSgMmaWarp) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool lead = sg_elect();
       int st = 0, i = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int u = unit; ok && walk.at(u, &t); u += units, i++) {
         const int nn = (t.n + 16 * CG - 1) / (16 * CG) * (16 * CG), buf = i & 1;
         const uint32_t idesc = sg_idesc(nn, kSgRows * CG), d = tmem + uint32_t(buf * a.acc_stride);
-        if (!(ok = tc_wait(&acc_empty[buf], uint32_t((i >> 1) & 1) ^ 1u, stop))) break;
+        if (!(ok = sg_wait(&acc_empty[buf], uint32_t((i >> 1) & 1) ^ 1u, stop))) break;
         tc_fence_after();
         for (int k = 0; k < kc; k++) {
-          if (!(ok = tc_wait(&full[st], ph, stop))) break;
+          if (!(ok = sg_wait(&full[st], ph, stop))) break;
           tc_fence_after();
-          const uint32_t wa = smem_u32(stages + size_t(st) * a.stage_bytes);
+          const uint32_t wa = smem_u32(stages) + uint32_t(st * a.stage_bytes);
           const uint64_t da = sg_desc(wa), db = sg_desc(wa + kSgWBytes);
-          // always the whole chunk (k past K reads as zero): four MMAs of 32 k issued back to back. With
-          // a loop over the pieces that K leaves, the issue alone took 219 cycles an MMA instead of 128
+          if (lead) {
+            // always the whole chunk (k past K reads as zero): four MMAs of 32 k issued back to back
 #pragma unroll
-          for (int j = 0; j < kSgChunk / 32; j++) sg_mma<CG>(d, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
-          sg_commit<CG>(&empty[st], 3u);
+            for (int j = 0; j < kSgChunk / 32; j++) sg_mma<CG>(d, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
+            sg_commit<CG>(&empty[st], 3u);
+            if (k == kc - 1) sg_commit<CG>(&acc_full[buf], 3u);
+          }
+          __syncwarp();
           if (++st == S) { st = 0; ph ^= 1; }
         }
-        if (ok) sg_commit<CG>(&acc_full[buf], 3u);
       }
-      if (!ok) give_up();
+      if (!ok && lead) give_up();
     }
   } else {
     pdl_wait();  // the tokens' scales may be the previous kernel's
@@ -850,7 +871,7 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
   constexpr bool FUSED = !std::is_same<T, int8_t>::value;
   extern __shared__ __align__(128) uint8_t ss_smem[];
   const uint32_t pad = (1024u - (smem_u32(ss_smem) & 1023u)) & 1023u;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = a.stages, P = a.splits;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), S = a.stages, P = a.splits;
   const uint32_t rank = P > 1 ? cluster_rank() : 0u;
   const int n0 = int(blockIdx.x) / P * kSgRows, kc = (a.K + kSgChunk - 1) / kSgChunk;
   const int k0 = int(rank) * kc / P, nk = (int(rank) + 1) * kc / P - k0;  // this CTA's chunks
@@ -870,7 +891,7 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
   uint32_t* most = reinterpret_cast<uint32_t*>(region + 512);
   uint32_t* stop = &words[1];
   const uint32_t bytes = kSgWBytes + (FUSED ? 0u : uint32_t(a.nn) * kSgChunk);
-  const bool copier = warp == kSgCopyWarp && lane == 0;
+  const bool copier = warp == kSgCopyWarp && sg_elect();
   auto copy_weights = [&](int j, int st) {
     mbar_expect_tx(&full[st], bytes);
     sg_copy_3d<1>(stages + size_t(st) * a.stage_bytes, &a.wmap, (k0 + j) * kSgChunk, n0, 0, smem_u32(&full[st]));
@@ -918,49 +939,52 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
   // before a peer is written to. Relaxed: a release here waits for the copies in flight, 2 us when the
   // memory is busy with weights.
   if (P > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
-  const uint32_t tmem = words[0];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, words[0], 0);
   pdl_wait();
   pdl_trigger();  // only now: what follows may count on everything before this kernel being complete
 
   if (warp == kSgCopyWarp) {
-    if (lane == 0) {
-      bool ok = true;
-      int j = 0, st = 0;
-      uint32_t ph = 1;
-      for (; j < nk; j++) {
-        if (j >= first) {
-          if (!(ok = tc_wait(&empty[st], ph, stop))) break;
-          copy_weights(j, st);
-        }
+    bool ok = true;
+    int j = 0, st = 0;
+    uint32_t ph = 1;
+    for (; j < nk; j++) {
+      if (j >= first && !(ok = sg_wait(&empty[st], ph, stop))) break;
+      if (copier) {
+        if (j >= first) copy_weights(j, st);
         copy_tokens(j, st);
-        if (++st == S) { st = 0; ph ^= 1; }
       }
+      __syncwarp();
+      if (++st == S) { st = 0; ph ^= 1; }
+    }
+    if (copier) {
       if (!ok) *reinterpret_cast<volatile uint32_t*>(stop) = 1u;
       words[2] = uint32_t(j);
-      for (int i = 0; i < first && ok; i++) {  // every stage's MMAs have arrived before this CTA may end
-        if (--st < 0) { st = S - 1; ph ^= 1; }
-        ok = tc_wait(&empty[st], ph ^ 1u, stop);
-      }
+    }
+    for (int i = 0; i < first && ok; i++) {  // every stage's MMAs have arrived before this CTA may end
+      if (--st < 0) { st = S - 1; ph ^= 1; }
+      ok = sg_wait(&empty[st], ph ^ 1u, stop);
     }
   } else if (warp == kSgMmaWarp) {
-    if (lane == 0) {
-      const uint32_t idesc = sg_idesc(a.nn, kSgRows);
-      bool ok = !FUSED || tc_wait(tok_full, 0, stop);
-      int st = 0;
-      uint32_t ph = 0;
-      for (int j = 0; j < nk && ok; j++) {
-        if (!(ok = tc_wait(&full[st], ph, stop))) break;
-        tc_fence_after();
-        const uint32_t wa = smem_u32(stages + size_t(st) * a.stage_bytes);
-        const uint64_t da = sg_desc(wa), db = sg_desc(FUSED ? smem_u32(operand) + uint32_t(j) * kSsFusedRow : wa + kSgWBytes);
+    const bool lead = sg_elect();
+    const uint32_t idesc = sg_idesc(a.nn, kSgRows);
+    bool ok = !FUSED || sg_wait(tok_full, 0, stop);
+    int st = 0;
+    uint32_t ph = 0;
+    for (int j = 0; j < nk && ok; j++) {
+      if (!(ok = sg_wait(&full[st], ph, stop))) break;
+      tc_fence_after();
+      const uint32_t wa = smem_u32(stages) + uint32_t(st * a.stage_bytes);
+      const uint64_t da = sg_desc(wa), db = sg_desc(FUSED ? smem_u32(operand) + uint32_t(j) * kSsFusedRow : wa + kSgWBytes);
+      if (lead) {
 #pragma unroll
         for (int i = 0; i < kSgChunk / 32; i++) sg_mma<1>(tmem, da + 2 * i, db + 2 * i, idesc, j > 0 || i > 0);
         tc_commit(&empty[st]);
-        if (++st == S) { st = 0; ph ^= 1; }
+        if (j == nk - 1) tc_commit(acc_full);
       }
-      if (ok) tc_commit(acc_full);
-      else *reinterpret_cast<volatile uint32_t*>(stop) = 1u;
+      __syncwarp();
+      if (++st == S) { st = 0; ph ^= 1; }
     }
+    if (!ok && lead) *reinterpret_cast<volatile uint32_t*>(stop) = 1u;
   } else {
     const int n = n0 + tid;  // this thread's channel
     const bool live = n < a.N;
