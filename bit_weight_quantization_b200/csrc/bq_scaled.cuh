@@ -162,7 +162,8 @@ __device__ __forceinline__ void sq_finish(const SqArgs& a, int i, const SqScale&
 template <typename T, bool GATE, int C, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) k_scaled_quantize(const SqArgs a) {
   __shared__ uint32_t most[32];
-  pdl_trigger();
+  pdl_wait();     // nothing is read or written before everything ahead is complete, and only then may the
+  pdl_trigger();  // next kernel start: its fetches ahead of its own wait can count on that
   const int i = int(blockIdx.x * blockDim.y + threadIdx.y);
   const bool live = i < a.M;
   bool bad = false;
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_scaled_quantize(const SqArgs a) 
 template <typename T, bool GATE>
 __global__ void __launch_bounds__(1024) k_scaled_quantize_long(const SqArgs a) {
   __shared__ uint32_t most[32];
+  pdl_wait();
   pdl_trigger();
   const int i = blockIdx.x;
   bool bad;
@@ -272,7 +274,7 @@ struct SgArgs {
   int w_experts;                   // distinct weight matrices: E, or 1 where the experts share one
   int bn;                          // tokens per tile at most, a multiple of 16 CG
   int stages, stage_bytes, cols, acc_stride;  // tensor-memory columns, and between accumulators
-  int splits;                      // CTAs that share a tile's k-range (split kernel)
+  int ahead;                       // the kernel before this one is the quantization: weights may be fetched before it ends
 };
 
 // Shared-memory descriptor of a K-major operand in 128-byte swizzled rows: start address, 1024
@@ -609,8 +611,9 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
       sg_copy_3d<CG>(stages + size_t(i) * a.stage_bytes, &a.wmap, k * kSgChunk, t.n0 + int(rank) * kSgRows,
                      min(t.e, a.w_experts - 1), bar_of(i));
     };
-    // the weights are constant: the first stages' are fetched before the wait for the kernel that
-    // makes the tokens' codes (a whole product's tiles do not hang on device data)
+    // behind the quantization (which waits for everything before it) the first stages' weights are
+    // fetched while it runs; a whole product's tiles do not hang on device data
+    if (!a.ahead) pdl_wait();
     if (!a.offsets && walk.at(unit, &t)) {
       ahead = min(S, kc);
       if (lead)
@@ -676,6 +679,7 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
     }
   } else {
     pdl_wait();  // the tokens' scales may be the previous kernel's
+    pdl_trigger();
     bool ok = true;
     const uint32_t lanes = uint32_t(32 * warp) << 16;
     uint8_t* ystage = stages + size_t(S) * a.stage_bytes + warp * 4096;

@@ -45,9 +45,8 @@ inline bool rows_aligned(const void* p, int type, int64_t ld) {
 template <typename T, bool GATE, int C, int MAXT, int MINB>
 inline cudaError_t launch_scaled_rows(const SqArgs& a, cudaStream_t s) {
   const int runs = (a.K + 7) / 8, per_row = ((runs + C - 1) / C + 31) / 32 * 32, rows = std::max(1, 256 / per_row);
-  k_scaled_quantize<T, GATE, C, MAXT, MINB>
-      <<<unsigned((a.M + (long long)rows - 1) / rows), dim3(unsigned(per_row), unsigned(rows)), 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(k_scaled_quantize<T, GATE, C, MAXT, MINB>, dim3(unsigned((a.M + (long long)rows - 1) / rows)),
+                    dim3(unsigned(per_row), unsigned(rows)), 0, s, a);
 }
 
 // Runs of 8 elements a thread. Few rows are spread over as many threads as they fill (64 rows of 11008
@@ -56,10 +55,7 @@ inline cudaError_t launch_scaled_rows(const SqArgs& a, cudaStream_t s) {
 template <typename T, bool GATE>
 inline cudaError_t launch_scaled_quantize(const SqArgs& a, cudaStream_t s) {
   const int runs = (a.K + 7) / 8;
-  if (runs > 4096) {
-    k_scaled_quantize_long<T, GATE><<<unsigned(a.M), 1024, 0, s>>>(a);
-    return cudaGetLastError();
-  }
+  if (runs > 4096) return launch_pdl(k_scaled_quantize_long<T, GATE>, dim3(unsigned(a.M)), dim3(1024), 0, s, a);
   if ((long long)a.M * runs <= 148 * 1024 || runs <= 64) {
     if (runs <= 1024) return launch_scaled_rows<T, GATE, 1, 1024, 1>(a, s);
     if (runs <= 2048) return launch_scaled_rows<T, GATE, 2, 1024, 1>(a, s);
@@ -114,12 +110,33 @@ inline bool encode_output_map(void* y, int64_t ldy, int M, int N, TcTensorMap* o
   return true;
 }
 
+// shared memory of a CTA that leaves room for a second one on its SM
+constexpr uint32_t kSsSmem = 113 * 1024;
+
 struct SgPlan {
   int cg, bn, stages;
   uint32_t smem;
 };
 
-inline SgPlan plan_scaled_gemm(int M, int E, bool grouped, bool y_tma) {
+// Tokens per tile of CTA pairs, for rows of one product (or one expert) on N channels: the choice that
+// takes the fewest cycles by this model. A chunk of 128 k costs a pair its four MMAs (530 cycles at 256
+// tokens, 280 from 128 down) or the copies of its operands at 64 bytes a cycle and SM; a wave is as many
+// tiles as there are pairs; the last tile's epilogue, 23 cycles a token, is not hidden. (Measured, 333 x
+// 5120 x 5104: 21.9 us with 256, 17.9 with 128; 256 x 4096 x 4096: 16.8 and, with 64, 11.4.)
+inline int scaled_pair_tokens(long long rows, int groups, int N, int K) {
+  const long long nt = (N + 2 * kSgRows - 1) / (2 * kSgRows), kc = (K + kSgChunk - 1) / kSgChunk, pairs = sm_count() / 2;
+  int best = 256;
+  double best_cost = -1;
+  for (int bn = 256; bn >= 64; bn -= 32) {
+    const long long tiles = (rows + bn - 1) / bn * groups * nt, waves = (tiles + pairs - 1) / pairs;
+    const double chunk = std::max(4.0 * std::max(70.0, 0.52 * bn), (double(kSgWBytes) + 64.0 * bn) / 64.0);
+    const double cost = double(waves) * double(kc) * chunk + 23.0 * double(std::min<long long>(bn, rows));
+    if (best_cost < 0 || cost < best_cost) { best = bn; best_cost = cost; }
+  }
+  return best;
+}
+
+inline SgPlan plan_scaled_gemm(int M, int N, int K, int E, bool grouped, bool y_tma) {
   SgPlan p{};
   const long long rows = grouped ? ((long long)M + E - 1) / E : M;  // of one expert, on average
   const long long most = grouped ? std::min<long long>(M, 2 * rows) : M;
@@ -128,17 +145,19 @@ inline SgPlan plan_scaled_gemm(int M, int E, bool grouped, bool y_tma) {
     p.bn = int(std::min<long long>(64, (most + 15) / 16 * 16));
   } else {
     p.cg = 2;
-    p.bn = int(std::min<long long>(256, (most + 31) / 32 * 32));
+    p.bn = int(std::min<long long>(grouped ? 256 : scaled_pair_tokens(rows, 1, N, K), (most + 31) / 32 * 32));
   }
   const uint32_t stage = kSgWBytes + uint32_t(p.bn / p.cg) * kSgChunk;
   const uint32_t fixed = 1024 + kSgRegion + (y_tma ? kSgYBytes : 0u) + (grouped ? 4u * uint32_t(E + 1) : 0u);
-  p.stages = std::min(kSgMaxStages, int((kTcSmemMax - fixed) / stage));
+  // single CTAs (few rows an expert) leave room for the next launch's beside them
+  const uint32_t room = p.cg == 1 ? kSsSmem : kTcSmemMax;
+  p.stages = std::min(kSgMaxStages, int((room - fixed) / stage));
   p.smem = fixed + uint32_t(p.stages) * stage;
   return p;
 }
 
 template <int CG>
-inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long tiles, bool after_quantize, cudaStream_t s) {
+inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long tiles, cudaStream_t s) {
   auto k = k_scaled_tc<CG>;
   static std::mutex mu;
   static unsigned long long set_ctx = 0;
@@ -166,12 +185,8 @@ inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long ti
     at[n].val.clusterDim.y = 1;
     at[n++].val.clusterDim.z = 1;
   }
-  // Only behind this library's own quantization, itself launched without the attribute: everything
-  // before it, the weights' last writer among it, is then complete when this kernel fetches weights.
-  if (after_quantize) {
-    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
+  at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[n++].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = n;
   if (cudaLaunchKernelEx(&cfg, k, a) != cudaSuccess) {
@@ -184,7 +199,6 @@ inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long ti
 // The split kernel for M tokens (M <= kSsMaxTokens): clusters of `splits` CTAs per 128 channels, each
 // CTA within half of an SM's shared memory. Two then run on an SM, or one beside the next launch's first
 // (with the whole of it, one token of 4096 x 4096 took 9.7 us among others instead of 6.6).
-constexpr uint32_t kSsSmem = 113 * 1024;
 
 // What p splits are expected to take, in ns, with `active` CTAs of `stages` stages at work: a chunk of 16 KB
 // of weights per CTA and latency / stages (1.5 us, 2.3 where two CTAs share an SM), but no faster than
@@ -324,7 +338,7 @@ inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_
   }
   // 16-bit outputs leave by TMA where their rows start on 16-byte boundaries
   const bool y_tma = y_type != BQ_TYPE_F32 && rows_aligned(y, y_type, ldy);
-  const SgPlan p = plan_scaled_gemm(M, w->experts, grouped, y_tma);
+  const SgPlan p = plan_scaled_gemm(M, w->N, w->K, w->experts, grouped, y_tma);
   const int channels = kSgRows * p.cg;
   const long long tiles = ((long long)(M + p.bn - 1) / p.bn + (grouped ? w->experts : 0)) * ((w->N + channels - 1) / channels);
   if (tiles > (1 << 30)) return BQ_ERR_SIZE;
@@ -335,13 +349,13 @@ inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_
       !encode_codes_map(q, ldq, M, w->K, 0, 0, 16, &a.qmap16) || (y_tma && !encode_output_map(y, ldy, M, w->N, &a.ymap)))
     return BQ_ERR_CUDA;
   a.w_scale = w->scale; a.bias = w->bias; a.scale = scale; a.offsets = offsets; a.y = y; a.ldy = ldy;
-  a.M = M; a.N = w->N; a.K = w->K; a.E = w->experts; a.y_type = y_type; a.y_tma = y_tma;
+  a.M = M; a.N = w->N; a.K = w->K; a.E = w->experts; a.y_type = y_type; a.y_tma = y_tma; a.ahead = after_quantize;
   a.bn = p.bn; a.stages = p.stages; a.stage_bytes = int(kSgWBytes) + p.bn / p.cg * kSgChunk;
   a.acc_stride = (p.bn + 31) / 32 * 32;
   a.cols = 32;
   while (a.cols < 2 * a.acc_stride) a.cols *= 2;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return p.cg == 2 ? launch_scaled_tc<2>(a, p, tiles, after_quantize, s) : launch_scaled_tc<1>(a, p, tiles, after_quantize, s);
+  return p.cg == 2 ? launch_scaled_tc<2>(a, p, tiles, s) : launch_scaled_tc<1>(a, p, tiles, s);
 }
 
 }  // namespace bqi
