@@ -649,6 +649,7 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
       ok = sg_wait(&empty[st], ph ^ 1u, stop);
     }
   } else if (warp == kSgMmaWarp) {
+    pdl_wait();  // not in the bounded waits below: the kernel before may take any time
     if (rank == 0) {
       const bool lead = sg_elect();
       int st = 0, i = 0;

@@ -149,7 +149,7 @@ inline SgPlan plan_scaled_gemm(int M, int N, int K, int E, bool grouped, bool y_
   }
   const uint32_t stage = kSgWBytes + uint32_t(p.bn / p.cg) * kSgChunk;
   const uint32_t fixed = 1024 + kSgRegion + (y_tma ? kSgYBytes : 0u) + (grouped ? 4u * uint32_t(E + 1) : 0u);
-  // single CTAs (few rows an expert) leave room for the next launch's beside them
+  // single CTAs (few rows an expert) share an SM
   const uint32_t room = p.cg == 1 ? kSsSmem : kTcSmemMax;
   p.stages = std::min(kSgMaxStages, int((room - fixed) / stage));
   p.smem = fixed + uint32_t(p.stages) * stage;
@@ -173,7 +173,10 @@ inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long ti
     }
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(CG * std::min<long long>(tiles, sm_count() / CG)));
+  // one CTA pair per two SMs, or two single CTAs an SM (64 rows of 64 experts, 2048 x 2048: 39.5 us with one,
+  // 37.4 with two; 2000 rows: 55.3 and 47.1)
+  const int ctas = CG == 2 ? sm_count() / 2 * 2 : 2 * sm_count();
+  cfg.gridDim = dim3(unsigned(std::min<long long>(CG * tiles, ctas)));
   cfg.blockDim = dim3(kSgThreads);
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = s;
@@ -306,8 +309,9 @@ inline bq_status launch_scaled_fused(const SsArgs& a, cudaStream_t s) {
   return a.M == 1 ? launch_scaled_split<T, 1>(a, s) : a.M == 2 ? launch_scaled_split<T, 2>(a, s) : launch_scaled_split<T, 4>(a, s);
 }
 
-// Whether bq_scaled_linear quantizes inside the product: up to kSsFusedTokens tokens, and the codes of
-// one CTA's k-range (of at most 1/8 of K where it is long) within 32 KB
+// Whether bq_scaled_linear quantizes inside the product: up to kSsFusedTokens tokens (4 of 4096 x 4096: 9.5 us
+// in one launch, 8 in two: 7.9, but every launch costs its caller 3 to 4 us), and K <= 16384 so that the
+// operand of any split leaves room for stages.
 inline bool scaled_fused(int M, int K) { return M <= kSsFusedTokens && K <= 16384; }
 
 inline bool split_args(const bq_scaled_weights* w, int M, void* y, int y_type, int64_t ldy, SsArgs* a) {
@@ -404,7 +408,7 @@ bq_status bq_scaled_workspace_bytes(const bq_scaled_weights* w, int32_t M, size_
   if (st != BQ_OK) return st;
   if (!bytes) return BQ_ERR_INVALID_ARG;
   if (M < 0 || M > kSgMaxM) return BQ_ERR_SIZE;
-  *bytes = size_t(align256(uint64_t(M) * scaled_ld(w->K)) + align256(4ull * M));
+  *bytes = scaled_fused(M, w->K) ? 0 : size_t(align256(uint64_t(M) * scaled_ld(w->K)) + align256(4ull * M));
   return BQ_OK;
 }
 
@@ -418,7 +422,7 @@ bq_status bq_scaled_linear(const bq_scaled_weights* w, const void* x, int32_t x_
   if (M == 0) return BQ_OK;
   if ((st = check_values(x, x_type, ldx, w->K)) != BQ_OK) return st;
   if ((st = check_values(y, y_type, ldy, w->N)) != BQ_OK) return st;
-  if (!workspace || !aligned(workspace, 256)) return BQ_ERR_INVALID_ARG;
+  if (need > 0 && (!workspace || !aligned(workspace, 256))) return BQ_ERR_INVALID_ARG;
   if (workspace_bytes < need) return BQ_ERR_SIZE;
   if (scaled_fused(M, w->K)) {
     SsArgs a{};

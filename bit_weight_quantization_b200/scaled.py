@@ -137,6 +137,7 @@ class ScaledLinear:
         self.experts, self.N, self.K = E, N, K
         self.weights = bq.bq_scaled_weights(c3.data_ptr(), sp, bp, sn, se, N, K, E)
         self._w = ctypes.byref(self.weights)
+        self._workspace = {}  # tokens -> workspace bytes (sizes only; the memory is allocated per call)
 
     @classmethod
     def quantize(cls, W, bias=None):
@@ -173,10 +174,12 @@ class ScaledLinear:
             with _on(dev, stream):
                 return self.linear(x, y, dtype)
         y, kind, ldy = self._out(y, M, dtype or x.dtype, where)
-        n = (M * _up(self.K) + 255 & -256) + (4 * M + 255 & -256)  # bq_scaled_workspace_bytes
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        st = _linear(self._w, x.data_ptr(), _TYPE[x.dtype], ldx, M, y.data_ptr(), kind, ldy, ws.data_ptr(), n,
-                     _raw_stream(dev.index))
+        n = self._workspace.get(M)
+        if n is None:
+            n = self._workspace[M] = bq.bq_scaled_workspace_bytes(self.weights, M)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        st = _linear(self._w, x.data_ptr(), _TYPE[x.dtype], ldx, M, y.data_ptr(), kind, ldy,
+                     ws.data_ptr() if n else None, n, _raw_stream(dev.index))
         if st:
             raise bq.BQError(st, "bq_scaled_linear")
         return y

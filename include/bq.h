@@ -398,6 +398,9 @@ bq_status bq_scaled_quantize(const void* x, int32_t x_type, int64_t ldx, int32_t
 bq_status bq_scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_t ldq, const float* scale, int32_t M,
                          void* y, int32_t y_type, int64_t ldy, void* stream);
 
+/* Launches: every scaled call is launched with programmatic dependent launch, waits for the work
+ * before it before it touches memory, and lets the next kernel start only after that. */
+
 /* bq_scaled_gemm with expert e's weights for the rows offsets[e] <= m < offsets[e+1]; `offsets`
  * (device int32 [experts + 1]) is read by the kernel, so no host synchronization is needed and a
  * captured graph follows its contents. 0 <= offsets[0] <= offsets[1] <= ... <= M; experts may be
@@ -407,8 +410,10 @@ bq_status bq_scaled_gemm_grouped(const bq_scaled_weights* w, const int8_t* q, in
                                  int32_t M, const int32_t* offsets, void* y, int32_t y_type, int64_t ldy,
                                  void* stream);
 
-/* bq_scaled_quantize of x [M][K] into `workspace` (device, 256-byte aligned, at least
- * bq_scaled_workspace_bytes), then bq_scaled_gemm from it: same results as the two calls. */
+/* bq_scaled_quantize of x [M][K], then bq_scaled_gemm: the same results as the two calls. Up to 4 tokens
+ * with K <= 16384 are quantized inside the product, in one launch; otherwise the codes and scales go
+ * through `workspace` (device, 256-byte aligned, at least bq_scaled_workspace_bytes; it may be NULL
+ * where that is 0), which the call writes before it reads. */
 bq_status bq_scaled_workspace_bytes(const bq_scaled_weights* w, int32_t M, size_t* bytes);
 bq_status bq_scaled_linear(const bq_scaled_weights* w, const void* x, int32_t x_type, int64_t ldx, int32_t M,
                            void* y, int32_t y_type, int64_t ldy, void* workspace, size_t workspace_bytes,

@@ -180,7 +180,8 @@ SHAPES = [(1, 1, 1), (1, 16, 16), (3, 7, 5), (1, 4096, 4096), (2, 128, 128), (7,
           (17, 1000, 33), (31, 512, 2049), (32, 64, 4096), (33, 255, 640), (63, 130, 129), (64, 2048, 2048),
           (65, 257, 127), (96, 96, 96), (127, 384, 1111), (128, 128, 128), (129, 640, 512), (200, 1025, 300),
           (256, 256, 256), (257, 257, 257), (300, 300, 5111), (333, 5120, 640), (512, 513, 64), (1000, 100, 100),
-          (1, 13824, 5120), (5, 11008, 4096), (24, 40, 16400), (2049, 300, 130)]
+          (1, 13824, 5120), (5, 11008, 4096), (24, 40, 16400), (2049, 300, 130), (100, 16, 64), (70, 8, 32), (100, 24, 200),
+          (64, 13824, 256), (8, 300, 4096), (9, 300, 4096), (33, 128, 100), (64, 128, 130), (3, 70, 65536)]
 
 
 @pytest.mark.parametrize("name", KINDS)
@@ -501,6 +502,81 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         y_ref, p = grouped_ref(c, off)
         check(bq, y, y_ref, p, "fp32", False)
+    bq.bq_device_check()
+
+
+def test_calls_see_what_the_call_before_them_wrote():
+    """Weights, tokens and scales written on the stream right before every call, in launches that may overlap:
+    the products of every step are those of that step's values."""
+    torch, bq = mods()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    N, K = 512, 2048
+    q, s = bq.scaled_quantize(torch.zeros(N, K, device="cuda"))
+    layer = bq.ScaledLinear(q, s)
+    off = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    grouped = bq.ScaledLinear(q[None], s[None])
+    Ws = [torch.randn(N, K, generator=g, device="cuda") for _ in range(6)]
+    xs = {M: [torch.randn(M, K, generator=g, device="cuda") for _ in range(6)] for M in (1, 4, 20, 40, 200)}
+    got = []
+    for i, W in enumerate(Ws):
+        for M in (1, 4, 20, 200):
+            bq.scaled_quantize(W, q=q, scale=s)
+            got.append(layer.linear(xs[M][i]))
+            q.zero_()
+            bq.scaled_quantize(W, q=q, scale=s)
+            qx, sx = bq.scaled_quantize(xs[M][i])
+            got.append(layer.gemm(qx, sx, dtype=torch.float32))
+        bq.scaled_quantize(W, q=q, scale=s)
+        qx, sx = bq.scaled_quantize(xs[40][i])
+        got.append(grouped.gemm_grouped(qx, sx, off, dtype=torch.float32))
+    torch.cuda.synchronize()
+    it = iter(got)
+    for i, W in enumerate(Ws):
+        w, sw = R.quantize(host(W))
+        sw = (np.abs(host(W)).max(1) / np.float32(127)).astype(np.float32)
+        for M in (1, 4, 20, 200, 40):
+            x = host(xs[M][i])
+            qr, _ = R.quantize(x)
+            y_ref, p = R.gemm(qr, (np.abs(x).max(1) / np.float32(127)).astype(np.float32), w, sw)
+            for _ in range(1 if M == 40 else 2):
+                check(bq, next(it), y_ref, p, "fp32", False)
+
+
+def test_results_are_the_same_every_time():
+    """Split sums, atomics-free: the same bits from every run, alone and among others."""
+    torch, bq = mods()
+    rng = np.random.default_rng(6)
+    w, wd = codes(torch, rng, 640, 4096)
+    sw, swd = scales(torch, rng, 640)
+    layer = bq.ScaledLinear(wd, swd)
+    for M in (1, 3, 8, 9, 33, 64, 65, 300):
+        x = torch.randn(M, 4096, device="cuda")
+        first = layer.linear(x)
+        torch.cuda.synchronize()
+        many = [layer.linear(x) for _ in range(30)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(first, y) for y in many), M
+    bq.bq_device_check()
+
+
+def test_beside_the_packed_layers():
+    """Scaled and packed layers alternating on one stream: each as it is alone."""
+    torch, bq = mods()
+    g = torch.Generator(device="cuda").manual_seed(8)
+    W = torch.randn(256, 1024, generator=g, device="cuda")
+    packed = [bq.QuantLinear("abq", W, w_bits=8, a_bits=8), bq.QuantLinear("bitnet", W)]
+    scaled = bq.ScaledLinear.quantize(W)
+    for M in (1, 16, 40):
+        x = torch.randn(M, 1024, generator=g, device="cuda").bfloat16()
+        calls = [lambda: packed[0].linear(x), lambda: scaled.linear(x), lambda: packed[1].linear(x), lambda: scaled.linear(x)]
+        alone = []
+        for c in calls:
+            torch.cuda.synchronize()
+            alone.append(c())
+        torch.cuda.synchronize()
+        rows = [[c() for c in calls] for _ in range(20)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, y) for r in rows for a, y in zip(alone, r))
     bq.bq_device_check()
 
 

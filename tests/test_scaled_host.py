@@ -88,13 +88,13 @@ def test_offsets_and_expert_counts():
     assert bq.raw_status("bq_scaled_linear", one, None, 1, 0, 0, None, 1, 0, None, 0, None) == OK
 
 
-LINEAR = dict(x=P, x_type=1, ldx=4096, M=4, y=P, y_type=1, ldy=64, ws=P, n=1 << 20)
+LINEAR = dict(x=P, x_type=1, ldx=4096, M=6, y=P, y_type=1, ldy=64, ws=P, n=1 << 20)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(x=None), INVALID), (dict(x=P + 1), INVALID), (dict(x_type=3), INVALID), (dict(ldx=4095), SIZE),
     (dict(M=-1), SIZE), (dict(y=None), INVALID), (dict(y_type=9), INVALID), (dict(ldy=10), SIZE),
-    (dict(ws=None), INVALID), (dict(ws=P + 128), INVALID), (dict(n=4 * 4096 + 255), SIZE)])
+    (dict(ws=None), INVALID), (dict(ws=P + 128), INVALID), (dict(n=6 * 4096 + 255), SIZE)])
 def test_bad_linear_arguments(kw, status):
     a = {**LINEAR, **kw}
     assert bq.raw_status("bq_scaled_linear", ctypes.byref(weights()), *[a[k] for k in LINEAR], None) == status
@@ -117,7 +117,10 @@ def test_bad_quantize_arguments(kw, status):
 def test_workspace_bytes():
     w = weights(K=4100, ld=4112)
     assert bq.bq_scaled_workspace_bytes(w, 0) == 0
-    for M in (1, 3, 64, 70000):
+    # up to four tokens are quantized inside the product
+    assert [bq.bq_scaled_workspace_bytes(w, M) for M in (1, 2, 3, 4)] == [0] * 4
+    assert bq.bq_scaled_workspace_bytes(weights(K=16385, ld=16400), 1) == 16640 + 256
+    for M in (5, 64, 70000):
         up = lambda v: (v + 255) // 256 * 256  # noqa: E731
         assert bq.bq_scaled_workspace_bytes(w, M) == up(M * 4112) + up(4 * M)
 
