@@ -90,14 +90,14 @@ def scaled_quantize(x, gate=None, rows=None, q=None, scale=None, stream=None):
         M = rows.shape[0] if rows.dim() == 1 else -1
         rp = _vector(rows, "rows", where, M, torch.int32, dev)
     if q is None:
-        q, ldq = empty_codes(M, K, dev), _up(K)
+        q, ldq = x.new_empty_strided((M, K), (_up(K), 1), dtype=torch.int8), _up(K)
     else:
         n, ldq = _matrix(q, "q", where, K, dev)
         if n != M or q.dtype != torch.int8:
             _refuse(where, f"q is {M} rows of int8")
         ldq = ldq if M > 1 else _up(K)
     if scale is None:
-        scale = torch.empty(M, dtype=torch.float32, device=dev)
+        scale = x.new_empty(M, dtype=torch.float32)
         sp = scale.data_ptr()
     else:
         sp = _vector(scale, "scale", where, M, torch.float32, dev)
@@ -152,7 +152,7 @@ class ScaledLinear:
         if y is None:
             if dtype not in _TYPE:
                 _refuse(where, f"y cannot have dtype {dtype}")
-            return torch.empty((M, self.N), dtype=dtype, device=self.device), _TYPE[dtype], self.N
+            return self.scale.new_empty((M, self.N), dtype=dtype), _TYPE[dtype], self.N
         n, ldy = _matrix(y, "y", where, self.N, self.device)
         if n != M or y.dtype not in _TYPE:
             _refuse(where, f"y is {M} rows of f32, bf16 or f16")
@@ -177,7 +177,7 @@ class ScaledLinear:
         n = self._workspace.get(M)
         if n is None:
             n = self._workspace[M] = bq.bq_scaled_workspace_bytes(self.weights, M)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        ws = x.new_empty(n, dtype=torch.uint8) if n else None
         st = _linear(self._w, x.data_ptr(), _TYPE[x.dtype], ldx, M, y.data_ptr(), kind, ldy,
                      ws.data_ptr() if n else None, n, _raw_stream(dev.index))
         if st:
