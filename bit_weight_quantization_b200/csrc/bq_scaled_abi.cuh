@@ -119,8 +119,8 @@ struct SgPlan {
 };
 
 // Tokens per tile of CTA pairs, for rows of one product (or one expert) on N channels: the choice that
-// takes the fewest cycles by this model. A chunk of 128 k costs a pair its four MMAs (530 cycles at 256
-// tokens, 280 from 128 down) or the copies of its operands at 64 bytes a cycle and SM; a wave is as many
+// takes the fewest cycles by this model. A chunk of 128 k costs a pair its four MMAs (138 cycles each at 256
+// tokens, 69 at 128, 47 at 64) or the copies of its operands at 64 bytes a cycle and SM; a wave is as many
 // tiles as there are pairs; the last tile's epilogue, 23 cycles a token, is not hidden. (Measured, 333 x
 // 5120 x 5104: 21.9 us with 256, 17.9 with 128; 256 x 4096 x 4096: 16.8 and, with 64, 11.4.)
 inline int scaled_pair_tokens(long long rows, int groups, int N, int K) {
@@ -129,7 +129,7 @@ inline int scaled_pair_tokens(long long rows, int groups, int N, int K) {
   double best_cost = -1;
   for (int bn = 256; bn >= 64; bn -= 32) {
     const long long tiles = (rows + bn - 1) / bn * groups * nt, waves = (tiles + pairs - 1) / pairs;
-    const double chunk = std::max(4.0 * std::max(70.0, 0.52 * bn), (double(kSgWBytes) + 64.0 * bn) / 64.0);
+    const double chunk = std::max(4.0 * std::max(47.0, 0.54 * bn), (double(kSgWBytes) + 64.0 * bn) / 64.0);
     const double cost = double(waves) * double(kc) * chunk + 23.0 * double(std::min<long long>(bn, rows));
     if (best_cost < 0 || cost < best_cost) { best = bn; best_cost = cost; }
   }
