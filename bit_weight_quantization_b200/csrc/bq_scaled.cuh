@@ -746,17 +746,17 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
 // order). The tensor cores keep up with the memory although an MMA of 128 channels costs the same
 // 27 ns for 16 tokens as for 64 (4 KB of weights: 150 GB/s an SM, 22 TB/s in all). Bound by the memory and
 // by the time until its first bytes: 1 x 4096 x 4096 from bf16 in 6.7 us (2.5 TB/s), 1 x 13824 x 5120 in
-// 14.8 (4.8 TB/s), 16 x 4096 x 4096 from codes in 6.1.
+// 14.7 (4.8 TB/s); from codes 16 x 4096 x 4096 in 6.1, 1 x 13824 x 5120 in 13.8 (5.1 TB/s).
 //
 // T = int8_t: the tokens' codes come by TMA beside the weights. Otherwise x is quantized here, by
 // every CTA the tokens of the whole row (their maximum) and the codes of its own k-range, straight
 // into the operand's swizzled rows, while the weights are on their way: one launch for a decoded token.
 
-constexpr int kSsMaxTokens = 64, kSsFusedTokens = 4;
+constexpr int kSsMaxTokens = 64, kSsFusedTokens = 2;
 constexpr int kSsMaxSplit = 8, kSsDirect = 8;
 constexpr uint32_t kSsFusedRow = 16 * kSgChunk;  // a chunk of the fused operand: 16 rows of 128 codes
 // after the stages, the fused operand and the received sums: full[12] (0), empty[12] (96), acc_full
-// (192), tok_full (200), sums_full (208), words[8] (224), token scales [64] (256), maxima [4][4] (512)
+// (192), tok_full (200), sums_full (208), words[8] (224), token scales [64] (256), maxima [2][4] (512)
 constexpr uint32_t kSsRegion = 576;
 
 struct SsArgs {
@@ -829,7 +829,7 @@ __device__ __forceinline__ void ss_ld4(uint32_t taddr, uint32_t (&v)[4]) {
 // take three times as long.
 template <typename T, int TOK>
 __device__ __forceinline__ void ss_maxima(const SsArgs& a, uint32_t* most, int tid) {
-  constexpr int U = (sizeof(T) == 4 ? 8 : 16) / TOK < 4 ? (sizeof(T) == 4 ? 8 : 16) / TOK : 4;
+  constexpr int U = 4;
   uint32_t m[TOK] = {};
   for (int k0 = 8 * tid; k0 == 8 * tid || k0 < a.K; k0 += 8 * 128 * U) {
     SqRun<T> h[U][TOK];

@@ -203,16 +203,26 @@ inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long ti
 // CTA within half of an SM's shared memory. Two then run on an SM, or one beside the next launch's first
 // (with the whole of it, one token of 4096 x 4096 took 9.7 us among others instead of 6.6).
 
-// What p splits are expected to take, in ns, with `active` CTAs of `stages` stages at work: a chunk of 16 KB
-// of weights per CTA and latency / stages (1.5 us, 2.3 where two CTAs share an SM), but no faster than
-// 6.3 TB/s for all; 3 us for launch, first copies and output; 0.25 us a CTA of the cluster and 20 ns a
-// token where there are sums to exchange. (Measured, in us: one token, 4096 x 4096: 6.6 in four, 7.2 in
-// eight; 13824 x 5120: 15.1 whole, 14.4 in two; 64 tokens: 4096 x 4096 16.5 whole, 9.8 in four;
-// 13824 x 5120 18.2 whole, 20.1 in two.)
-inline double scaled_split_ns(int p, int chunks, int stages, long long active, long long waves, int M) {
-  const double latency = active > sm_count() ? 2300.0 : 1500.0;
-  const double chunk = std::max(latency / stages, double(active) * kSgWBytes / 6300.0);
-  return double(waves) * (chunks * chunk + 3000.0) + 250.0 * p + (p > 1 ? 20.0 * M : 0.0);
+// What p splits of `tiles` 128-channel tiles are expected to take, in ns, where `clusters` of p CTAs run at
+// once. A chunk of k takes an SM 200 ns for 16 KB of weights (more with the tokens' codes beside them), or
+// 900 ns over the stages in flight; all SMs together draw at most 16 KB in 2.64 ns, 2.45 where two CTAs
+// share some. SMs take equal shares, so those with two CTAs finish their second one's chunks alone. 2 us for
+// a further wave, 2.7 for launch, first copies and output, and the exchange of the sums grows with the tokens;
+// a CTA that quantizes takes 0.1 us a chunk of its own range. (Measured, in us, for 1 / 2 / 3 / 4 / 6 / 8
+// splits: one token from codes, 4096 x 4096: 9.1 / 6.8 / 5.8 / 5.7 / 6.4 / 5.6; 11008 x 4096: 10.5 / 11.2 /
+// 9.4 / 12.0 / 12.3 / 13.2; 13824 x 5120: 13.8 / 13.9 / 16.1 / 15.0 / 17.6 / 17.7; 4096 x 11008: 20.7 / 12.5 /
+// 10.2 / 10.0 / 9.7 / 9.4; 64 tokens, 4096 x 4096: 13.3 / 12.2 / 9.7 / 9.1 / 9.8 / 9.2.)
+inline double scaled_split_ns(int p, int tiles, int clusters, int chunks, int stages, int stage_bytes, int M, bool fused) {
+  const double least = std::max(200.0 * stage_bytes / kSgWBytes, 900.0 / stages);
+  const int sms = sm_count();
+  auto wave = [&](int n) {  // n clusters at once
+    const int a = n * p;
+    if (a <= sms) return chunks * std::max(least, 2.64 * a);
+    return chunks * (std::max(least, 2.45 * sms) + std::max(least, 2.45 * (a - sms)));
+  };
+  const int full = tiles / clusters, rest = tiles % clusters;
+  return 2700.0 + full * wave(clusters) + (rest ? wave(rest) : 0.0) + 2000.0 * (full + (rest ? 1 : 0) - 1) +
+         (p > 1 ? 25.0 * M + 0.45 * M * M : 16.0 * M) + (fused ? 50.0 * chunks * (M + 1) : 0.0);
 }
 
 template <typename T, int TOK>
@@ -273,8 +283,7 @@ inline bq_status launch_scaled_split(SsArgs a, cudaStream_t s) {
     const uint32_t room = fixed + uint32_t(2 * t.stage_bytes) > kSsSmem ? kTcSmemMax : kSsSmem;
     if (fixed + uint32_t(least * t.stage_bytes) > room) continue;
     t.stages = std::min(std::max(least, std::min(kSgMaxStages, chunks)), int((room - fixed) / uint32_t(t.stage_bytes)));
-    const long long waves = (tiles + slots - 1) / slots, active = (long long)std::min(tiles, slots) * p;
-    const double ns = scaled_split_ns(p, chunks, t.stages, active, waves, a.M) + (room > kSsSmem ? 3000.0 : 0.0);
+    const double ns = scaled_split_ns(p, tiles, slots, chunks, t.stages, t.stage_bytes, a.M, FUSED) + (room > kSsSmem ? 5000.0 : 0.0);
     if (best < 0 || ns < best) {
       best = ns;
       run = t;
@@ -305,13 +314,13 @@ inline bq_status launch_scaled_split(SsArgs a, cudaStream_t s) {
 
 template <typename T>
 inline bq_status launch_scaled_fused(const SsArgs& a, cudaStream_t s) {
-  static_assert(kSsFusedTokens == 4, "instantiations");
-  return a.M == 1 ? launch_scaled_split<T, 1>(a, s) : a.M == 2 ? launch_scaled_split<T, 2>(a, s) : launch_scaled_split<T, 4>(a, s);
+  static_assert(kSsFusedTokens == 2, "instantiations");
+  return a.M == 1 ? launch_scaled_split<T, 1>(a, s) : launch_scaled_split<T, 2>(a, s);
 }
 
-// Whether bq_scaled_linear quantizes inside the product: up to kSsFusedTokens tokens (4 of 4096 x 4096: 9.5 us
-// in one launch, 8 in two: 7.9, but every launch costs its caller 3 to 4 us), and K <= 16384 so that the
-// operand of any split leaves room for stages.
+// Whether bq_scaled_linear quantizes inside the product: up to kSsFusedTokens tokens, as every CTA reads them
+// all (4096 x 4096: one token 6.7 us, two 7.3, four 8.8, in two launches 7.6; 13824 x 5120: one token 14.7, two
+// 16.0, four 23.2, in two launches 15.5), and K <= 16384 so that the operand of any split leaves room for stages.
 inline bool scaled_fused(int M, int K) { return M <= kSsFusedTokens && K <= 16384; }
 
 inline bool split_args(const bq_scaled_weights* w, int M, void* y, int y_type, int64_t ldy, SsArgs* a) {

@@ -410,7 +410,7 @@ bq_status bq_scaled_gemm_grouped(const bq_scaled_weights* w, const int8_t* q, in
                                  int32_t M, const int32_t* offsets, void* y, int32_t y_type, int64_t ldy,
                                  void* stream);
 
-/* bq_scaled_quantize of x [M][K], then bq_scaled_gemm: the same results as the two calls. Up to 4 tokens
+/* bq_scaled_quantize of x [M][K], then bq_scaled_gemm: the same results as the two calls. Up to 2 tokens
  * with K <= 16384 are quantized inside the product, in one launch; otherwise the codes and scales go
  * through `workspace` (device, 256-byte aligned, at least bq_scaled_workspace_bytes; it may be NULL
  * where that is 0), which the call writes before it reads. */

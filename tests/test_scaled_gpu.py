@@ -376,7 +376,7 @@ def test_experts_may_share_weights():
 # ---------------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("name", KINDS)
-@pytest.mark.parametrize("M,N,K", [(1, 300, 1000), (1, 4096, 4096), (1, 5, 3), (2, 64, 16384), (4, 2048, 2048),
+@pytest.mark.parametrize("M,N,K", [(1, 300, 1000), (1, 4096, 4096), (1, 5, 3), (2, 64, 16384), (2, 513, 4100), (1, 100, 16390), (4, 2048, 2048),
                                    (7, 77, 7777), (16, 1024, 640), (40, 512, 512), (130, 260, 1030), (513, 100, 256)])
 def test_linear_equals_quantize_and_gemm(M, N, K, name):
     torch, bq = mods()
