@@ -1069,17 +1069,17 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kSgMmaWarp) {
-    tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(a.cols) : "memory");
-  }
-  if (words[1]) {  // a role gave up: copies it had issued are given time to land, and peers to be done with it
+  if (words[1]) {  // a role gave up: copies and MMAs it had issued are given time to land
     if (tid == 0) {
       const int issued = max(int(words[2]), first);
       for (int j = max(0, issued - S); j < issued; j++) mbar_wait_bounded(&full[j % S], uint32_t((j / S) & 1));
       for (int j = 0; j < 1000; j++) __nanosleep(1000);
     }
     __syncthreads();
+  }
+  if (warp == kSgMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(a.cols) : "memory");
   }
   // no CTA leaves while its sums are being copied out of its shared memory; nor, if it did not get all that
   // it waited for, while a peer may still write to it (threads that have left count as arrived)
