@@ -6,6 +6,7 @@
 
 #include <type_traits>
 
+#include "bq_scaled_plan.h"
 #include "bq_tc.cuh"
 
 namespace bqi {
@@ -250,19 +251,8 @@ __global__ void __launch_bounds__(1024) k_scaled_quantize_long(const SqArgs a) {
 // Every wait is bounded and ends when another role has stopped; then the error word is raised,
 // the peer is told, copies in flight are waited for and the tensor memory is freed.
 
-constexpr int kSgRows = 128;       // channels per CTA
-constexpr int kSgChunk = 128;      // bytes of k per stage
 constexpr int kSgThreads = 192;
 constexpr int kSgCopyWarp = 4, kSgMmaWarp = 5;
-constexpr int kSgMaxStages = 12;
-constexpr int kSgMaxTokens = 256;  // tokens per tile at most
-constexpr uint32_t kSgWBytes = kSgRows * kSgChunk;
-// shared memory: alignment slack, the stages (each a multiple of 1024 bytes), the outputs'
-// staging where y is written by TMA, then this region:
-// full[12] (0), empty[12] (96), acc_full[2] (192), acc_empty[2] (208), words[8] (224), token scales
-// [2][256] (256); then, grouped, the first tile of every expert [E + 1]
-constexpr uint32_t kSgYBytes = 4 * 2 * 2048;  // outputs on their way: two blocks of 32 x 32 for each epilogue warp
-constexpr uint32_t kSgRegion = 256 + 2 * kSgMaxTokens * 4;
 
 struct SgArgs {
   TcTensorMap wmap, qmap, qmap16;  // weights; tokens in boxes of a whole tile, and of 16 rows
@@ -752,13 +742,6 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
 // every CTA the tokens of the whole row (their maximum) and the codes of its own k-range, straight
 // into the operand's swizzled rows, while the weights are on their way: one launch for a decoded token.
 
-constexpr int kSsMaxTokens = 64, kSsFusedTokens = 2;
-constexpr int kSsMaxSplit = 8, kSsDirect = 8;
-constexpr uint32_t kSsFusedRow = 16 * kSgChunk;  // a chunk of the fused operand: 16 rows of 128 codes
-// after the stages, the fused operand and the received sums: full[12] (0), empty[12] (96), acc_full
-// (192), tok_full (200), sums_full (208), words[8] (224), token scales [64] (256), maxima [2][4] (512)
-constexpr uint32_t kSsRegion = 576;
-
 struct SsArgs {
   TcTensorMap wmap, qmap;  // boxes of 128 channels, and of nn tokens
   SqArgs x;                // T != int8_t: the unquantized tokens
@@ -911,6 +894,11 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
       sg_copy_2d<1>(stages + size_t(st) * a.stage_bytes + kSgWBytes, &a.qmap, (k0 + j) * kSgChunk, 0, smem_u32(&full[st]));
   };
 
+  auto free_tmem = [&]() {  // by the whole MMA warp
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(words[0]), "r"(a.cols) : "memory");
+  };
+
   const int first = min(S, nk);
   if (copier) {  // before any other setup: the weights' first copies
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&a.wmap)) : "memory");
@@ -924,6 +912,15 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
     fence_mbar_init();
     if (P > 1) mbar_expect_tx(sums_full, uint32_t(P * max(0, min(a.slice, a.M - int(rank) * a.slice))) * kSgRows * 4u);
     if (!FUSED && !a.ahead) pdl_wait();
+  }
+  // Arrived once this CTA's barriers are set up (fence_mbar_init orders that for the cluster), waited for
+  // before a peer is written to. Relaxed, and ahead of the copies: a release behind them waits for the copies in
+  // flight, 2 us when the memory is busy with weights. Ahead of the allocation, which waits while other kernels
+  // hold the SM's tensor memory: no CTA waits for a peer while it holds columns itself (they are freed before
+  // the peers' sums are waited for), so what holds them always comes to its end.
+  if (P > 1) {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
   }
   if (FUSED && warp == kSgCopyWarp) {
     pdl_wait();
@@ -945,13 +942,10 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // Arrived once this CTA's barriers are set up (fence_mbar_init orders that for the cluster), waited for
-  // before a peer is written to. Relaxed: a release here waits for the copies in flight, 2 us when the
-  // memory is busy with weights.
-  if (P > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
   const uint32_t tmem = __shfl_sync(0xffffffffu, words[0], 0);
   pdl_wait();
   pdl_trigger();  // only now: what follows may count on everything before this kernel being complete
+  bool freed = false;  // the MMA warp's: the tensor memory
 
   if (warp == kSgCopyWarp) {
     bool ok = true;
@@ -995,6 +989,10 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
       if (++st == S) { st = 0; ph ^= 1; }
     }
     if (!ok && lead) *reinterpret_cast<volatile uint32_t*>(stop) = 1u;
+    __syncwarp();
+    asm volatile("bar.sync 3, 160;\n" ::: "memory");  // the accumulators are read, or a role has stopped
+    freed = __all_sync(0xffffffffu, *reinterpret_cast<const volatile uint32_t*>(stop) == 0u);
+    if (freed) free_tmem();
   } else {
     const int n = n0 + tid;  // this thread's channel
     const bool live = n < a.N;
@@ -1011,18 +1009,25 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
     bool ok = __all_sync(0xffffffffu, tc_wait(acc_full, 0, stop));
     tc_fence_after();
     const uint32_t acc = tmem + (uint32_t(32 * warp) << 16);
+    auto accumulators_read = [&]() {
+      if (!ok && lane == 0) *reinterpret_cast<volatile uint32_t*>(stop) = 1u;
+      tc_fence_before();
+      __syncwarp();
+      asm volatile("bar.arrive 3, 160;\n" ::: "memory");
+    };
     if (P == 1) {
       for (int c = 0; ok && c < a.M; c += 4) {
         uint32_t v[4];
         ss_ld4(acc + uint32_t(c), v);
         if (live) ss_out(a, c, a.M - c, n, scale, sw, b, v);
       }
+      accumulators_read();
     } else {
       // token m's sums to CTA m / slice, at [this CTA][m % slice][channel] there
       if (a.M <= kSsDirect) {  // few: straight from the registers, and this CTA need not wait for their arrival
         uint32_t v[8];
         ss_ld8(acc, v);
-        __syncwarp();
+        accumulators_read();
         asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 #pragma unroll
         for (int i = 0; i < kSsDirect; i++) {
@@ -1040,6 +1045,7 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
 #pragma unroll
           for (int i = 0; i < 8; i++) mine[(c + i) * kSgRows + tid] = v[i];
         }
+        accumulators_read();
         fence_proxy_async();
         asm volatile("bar.sync 1, 128;\n" ::: "memory");
         asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
@@ -1077,10 +1083,7 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
     }
     __syncthreads();
   }
-  if (warp == kSgMmaWarp) {
-    tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(a.cols) : "memory");
-  }
+  if (warp == kSgMmaWarp && !freed) free_tmem();
   // no CTA leaves while its sums are being copied out of its shared memory; nor, if it did not get all that
   // it waited for, while a peer may still write to it (threads that have left count as arrived)
   if (P > 1 && (a.M > kSsDirect || words[1])) {

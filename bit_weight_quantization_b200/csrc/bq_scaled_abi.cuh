@@ -6,6 +6,7 @@
 
 namespace bqi {
 
+static_assert(kSgSmemMax == kTcSmemMax, "shared memory of a CTA");
 constexpr int kSgMaxM = 0x7FFFFFFF - (1 << 16);  // tile ends stay inside int32
 
 inline int type_bytes(int t) { return t == BQ_TYPE_F32 ? 4 : 2; }
@@ -110,52 +111,6 @@ inline bool encode_output_map(void* y, int64_t ldy, int M, int N, TcTensorMap* o
   return true;
 }
 
-// shared memory of a CTA that leaves room for a second one on its SM
-constexpr uint32_t kSsSmem = 113 * 1024;
-
-struct SgPlan {
-  int cg, bn, stages;
-  uint32_t smem;
-};
-
-// Tokens per tile of CTA pairs, for rows of one product (or one expert) on N channels: the choice that
-// takes the fewest cycles by this model. A chunk of 128 k costs a pair its four MMAs (138 cycles each at 256
-// tokens, 69 at 128, 47 at 64) or the copies of its operands at 64 bytes a cycle and SM; a wave is as many
-// tiles as there are pairs; the last tile's epilogue, 23 cycles a token, is not hidden. (Measured, 333 x
-// 5120 x 5104: 21.9 us with 256, 17.9 with 128; 256 x 4096 x 4096: 16.8 and, with 64, 11.4.)
-inline int scaled_pair_tokens(long long rows, int groups, int N, int K) {
-  const long long nt = (N + 2 * kSgRows - 1) / (2 * kSgRows), kc = (K + kSgChunk - 1) / kSgChunk, pairs = sm_count() / 2;
-  int best = 256;
-  double best_cost = -1;
-  for (int bn = 256; bn >= 64; bn -= 32) {
-    const long long tiles = (rows + bn - 1) / bn * groups * nt, waves = (tiles + pairs - 1) / pairs;
-    const double chunk = std::max(4.0 * std::max(47.0, 0.54 * bn), (double(kSgWBytes) + 64.0 * bn) / 64.0);
-    const double cost = double(waves) * double(kc) * chunk + 23.0 * double(std::min<long long>(bn, rows));
-    if (best_cost < 0 || cost < best_cost) { best = bn; best_cost = cost; }
-  }
-  return best;
-}
-
-inline SgPlan plan_scaled_gemm(int M, int N, int K, int E, bool grouped, bool y_tma) {
-  SgPlan p{};
-  const long long rows = grouped ? ((long long)M + E - 1) / E : M;  // of one expert, on average
-  const long long most = grouped ? std::min<long long>(M, 2 * rows) : M;
-  if (rows <= 64) {
-    p.cg = 1;
-    p.bn = int(std::min<long long>(64, (most + 15) / 16 * 16));
-  } else {
-    p.cg = 2;
-    p.bn = int(std::min<long long>(grouped ? 256 : scaled_pair_tokens(rows, 1, N, K), (most + 31) / 32 * 32));
-  }
-  const uint32_t stage = kSgWBytes + uint32_t(p.bn / p.cg) * kSgChunk;
-  const uint32_t fixed = 1024 + kSgRegion + (y_tma ? kSgYBytes : 0u) + (grouped ? 4u * uint32_t(E + 1) : 0u);
-  // single CTAs (few rows an expert) share an SM
-  const uint32_t room = p.cg == 1 ? kSsSmem : kTcSmemMax;
-  p.stages = std::min(kSgMaxStages, int((room - fixed) / stage));
-  p.smem = fixed + uint32_t(p.stages) * stage;
-  return p;
-}
-
 template <int CG>
 inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long tiles, cudaStream_t s) {
   auto k = k_scaled_tc<CG>;
@@ -199,32 +154,6 @@ inline bq_status launch_scaled_tc(const SgArgs& a, const SgPlan& p, long long ti
   return BQ_OK;
 }
 
-// The split kernel for M tokens (M <= kSsMaxTokens): clusters of `splits` CTAs per 128 channels, each
-// CTA within half of an SM's shared memory. Two then run on an SM, or one beside the next launch's first
-// (with the whole of it, one token of 4096 x 4096 took 9.7 us among others instead of 6.6).
-
-// What p splits of `tiles` 128-channel tiles are expected to take, in ns, where `clusters` of p CTAs run at
-// once. A chunk of k takes an SM 200 ns for 16 KB of weights (more with the tokens' codes beside them), or
-// 900 ns over the stages in flight; all SMs together draw at most 16 KB in 2.64 ns, 2.45 where two CTAs
-// share some. SMs take equal shares, so those with two CTAs finish their second one's chunks alone. 2 us for
-// a further wave, 2.7 for launch, first copies and output, and the exchange of the sums grows with the tokens;
-// a CTA that quantizes takes 0.1 us a chunk of its own range. (Measured, in us, for 1 / 2 / 3 / 4 / 6 / 8
-// splits: one token from codes, 4096 x 4096: 9.1 / 6.8 / 5.8 / 5.7 / 6.4 / 5.6; 11008 x 4096: 10.5 / 11.2 /
-// 9.4 / 12.0 / 12.3 / 13.2; 13824 x 5120: 13.8 / 13.9 / 16.1 / 15.0 / 17.6 / 17.7; 4096 x 11008: 20.7 / 12.5 /
-// 10.2 / 10.0 / 9.7 / 9.4; 64 tokens, 4096 x 4096: 13.3 / 12.2 / 9.7 / 9.1 / 9.8 / 9.2.)
-inline double scaled_split_ns(int p, int tiles, int clusters, int chunks, int stages, int stage_bytes, int M, bool fused) {
-  const double least = std::max(200.0 * stage_bytes / kSgWBytes, 900.0 / stages);
-  const int sms = sm_count();
-  auto wave = [&](int n) {  // n clusters at once
-    const int a = n * p;
-    if (a <= sms) return chunks * std::max(least, 2.64 * a);
-    return chunks * (std::max(least, 2.45 * sms) + std::max(least, 2.45 * (a - sms)));
-  };
-  const int full = tiles / clusters, rest = tiles % clusters;
-  return 2700.0 + full * wave(clusters) + (rest ? wave(rest) : 0.0) + 2000.0 * (full + (rest ? 1 : 0) - 1) +
-         (p > 1 ? 25.0 * M + 0.45 * M * M : 16.0 * M) + (fused ? 50.0 * chunks * (M + 1) : 0.0);
-}
-
 template <typename T, int TOK>
 inline bq_status launch_scaled_split(SsArgs a, cudaStream_t s) {
   constexpr bool FUSED = !std::is_same<T, int8_t>::value;
@@ -262,50 +191,24 @@ inline bq_status launch_scaled_split(SsArgs a, cudaStream_t s) {
     }
     std::memcpy(clusters, max_clusters, sizeof(clusters));
   }
-  const int tiles = (a.N + kSgRows - 1) / kSgRows, kc = (a.K + kSgChunk - 1) / kSgChunk;
-  a.nn = (a.M + 15) / 16 * 16;
-  a.cols = 32;
-  while (a.cols < a.nn) a.cols *= 2;
-  a.stage_bytes = int(kSgWBytes) + (FUSED ? 0 : a.nn * kSgChunk);
-  // the stages also hold the CTA's sums, 512 bytes a token, before they are copied: two at least beyond 32 tokens
-  const int least = a.M > 32 ? 2 : 1;
-  double best = -1;
-  uint32_t smem = 0;
-  SsArgs run = a;
-  for (int p = 1; p <= kSsMaxSplit && p <= kc; p++) {
-    if (clusters[p] <= 0) continue;
-    const int slots = 2 * clusters[p], chunks = (kc + p - 1) / p;
-    SsArgs t = a;
-    t.splits = p;
-    t.slice = (a.M + p - 1) / p;
-    const uint32_t fixed = 1024 + kSsRegion + (FUSED ? uint32_t(chunks) * kSsFusedRow : 0u) +
-                           (p > 1 ? uint32_t(p * t.slice) * kSgRows * 4u : 0u);
-    const uint32_t room = fixed + uint32_t(2 * t.stage_bytes) > kSsSmem ? kTcSmemMax : kSsSmem;
-    if (fixed + uint32_t(least * t.stage_bytes) > room) continue;
-    t.stages = std::min(std::max(least, std::min(kSgMaxStages, chunks)), int((room - fixed) / uint32_t(t.stage_bytes)));
-    const double ns = scaled_split_ns(p, tiles, slots, chunks, t.stages, t.stage_bytes, a.M, FUSED) + (room > kSsSmem ? 5000.0 : 0.0);
-    if (best < 0 || ns < best) {
-      best = ns;
-      run = t;
-      smem = fixed + uint32_t(t.stages * t.stage_bytes);
-    }
-  }
-  if (best < 0) return BQ_ERR_UNSUPPORTED;
+  const SsPlan p = plan_scaled_split(a.M, a.N, a.K, FUSED, clusters, sm_count());
+  a.nn = p.nn; a.cols = p.cols; a.splits = p.splits; a.slice = p.slice; a.stages = p.stages; a.stage_bytes = p.stage_bytes;
+  if (p.splits == 0) return BQ_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(tiles * run.splits));
+  cfg.gridDim = dim3(unsigned((a.N + kSgRows - 1) / kSgRows * p.splits));
   cfg.blockDim = dim3(kSgThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = p.smem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = unsigned(run.splits);
+  at[1].val.clusterDim.x = unsigned(p.splits);
   at[1].val.clusterDim.y = 1;
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = run.splits > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, k, run) != cudaSuccess) {
+  cfg.numAttrs = p.splits > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, k, a) != cudaSuccess) {
     (void)cudaGetLastError();
     return BQ_ERR_CUDA;
   }
@@ -351,7 +254,7 @@ inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_
   }
   // 16-bit outputs leave by TMA where their rows start on 16-byte boundaries
   const bool y_tma = y_type != BQ_TYPE_F32 && rows_aligned(y, y_type, ldy);
-  const SgPlan p = plan_scaled_gemm(M, w->N, w->K, w->experts, grouped, y_tma);
+  const SgPlan p = plan_scaled_gemm(M, w->N, w->K, w->experts, grouped, y_tma, sm_count());
   const int channels = kSgRows * p.cg;
   const long long tiles = ((long long)(M + p.bn - 1) / p.bn + (grouped ? w->experts : 0)) * ((w->N + channels - 1) / channels);
   if (tiles > (1 << 30)) return BQ_ERR_SIZE;
@@ -363,10 +266,7 @@ inline bq_status scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_
     return BQ_ERR_CUDA;
   a.w_scale = w->scale; a.bias = w->bias; a.scale = scale; a.offsets = offsets; a.y = y; a.ldy = ldy;
   a.M = M; a.N = w->N; a.K = w->K; a.E = w->experts; a.y_type = y_type; a.y_tma = y_tma; a.ahead = after_quantize;
-  a.bn = p.bn; a.stages = p.stages; a.stage_bytes = int(kSgWBytes) + p.bn / p.cg * kSgChunk;
-  a.acc_stride = (p.bn + 31) / 32 * 32;
-  a.cols = 32;
-  while (a.cols < 2 * a.acc_stride) a.cols *= 2;
+  a.bn = p.bn; a.stages = p.stages; a.stage_bytes = p.stage_bytes; a.cols = p.cols; a.acc_stride = p.acc_stride;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return p.cg == 2 ? launch_scaled_tc<2>(a, p, tiles, s) : launch_scaled_tc<1>(a, p, tiles, s);
 }
