@@ -334,6 +334,9 @@ __device__ __forceinline__ void sg_copy_3d(void* dst, const TcTensorMap* map, in
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+// Instructions that the whole warp takes together (.aligned: tcgen05.ld, alloc and dealloc, stmatrix, the named and
+// the cluster barriers) stand behind a __syncwarp() or a vote wherever lanes may have gone different ways before.
+//
 // One lane of a converged warp. The copying and the MMA warp run their loops with all lanes and let one
 // issue: addresses and descriptors then stay in uniform registers. From a branch that only lane 0 takes, an
 // MMA took 76 cycles to issue and a chunk of four 594, whatever its tokens.
@@ -486,8 +489,8 @@ __device__ __forceinline__ void sg_epilogue(const SgArgs& a, const SgTile& t, ui
         *turn ^= 1;
         // the copy that read this buffer two blocks ago is done
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;\n" ::: "memory");
-        sg_wait_ld();
         __syncwarp();
+        sg_wait_ld();
 #pragma unroll
         for (int i = 0; i < 4; i++) {
           const float2 s = *reinterpret_cast<const float2*>(tok + c + 8 * i + 2 * tt);
@@ -504,6 +507,7 @@ __device__ __forceinline__ void sg_epilogue(const SgArgs& a, const SgTile& t, ui
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) sg_store_2d(&a.ymap, ch, t.m0 + c, buf);
+        __syncwarp();
       }
     }
   }
@@ -521,6 +525,7 @@ __device__ __forceinline__ void sg_epilogue(const SgArgs& a, const SgTile& t, ui
       if (i < left) sg_put(y, BIAS ? __fmaf_rn(x, s, b) : __fmul_rn(x, s));
       y += a.ldy;
     }
+    __syncwarp();
   }
 }
 
@@ -682,6 +687,7 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
       const int buf = i & 1;
       float* tk = tok + buf * kSgMaxTokens;
       for (int j = tid; j < t.n; j += 128) tk[j] = __ldg(a.scale + t.m0 + j);
+      __syncwarp();
       const int ch = t.n0 + int(rank) * kSgRows + 32 * warp;
       asm volatile("bar.sync 1, 128;\n" ::: "memory");  // the scales are written (buffer i - 2 was read before tile i - 1's)
       ok = __all_sync(0xffffffffu, tc_wait(&acc_full[buf], uint32_t((i >> 1) & 1), stop));
@@ -823,7 +829,10 @@ __device__ __forceinline__ void ss_maxima(const SsArgs& a, uint32_t* most, int t
         if (t < a.M && k0 + u * 8 * 128 < a.K)
           h[u][t].load(static_cast<const T*>(a.x.x) + t * a.x.ldx, k0 + u * 8 * 128, a.K, a.x.vec_x != 0);
         else h[u][t].zero();
-    if (k0 == 8 * tid) asm volatile("bar.arrive 2, 160;\n" ::: "memory");
+    if (k0 == 8 * tid) {  // every lane's first pass
+      __syncwarp();
+      asm volatile("bar.arrive 2, 160;\n" ::: "memory");
+    }
 #pragma unroll
     for (int u = 0; u < U; u++)
 #pragma unroll
@@ -1005,6 +1014,7 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
     } else if (tid < a.M) {
       scale[tid] = __ldg(a.scale + tid);
     }
+    __syncwarp();
     asm volatile("bar.sync 1, 128;\n" ::: "memory");  // the scales are written
     bool ok = __all_sync(0xffffffffu, tc_wait(acc_full, 0, stop));
     tc_fence_after();
@@ -1020,6 +1030,7 @@ __global__ void __launch_bounds__(kSgThreads, 2) k_scaled_split(const __grid_con
         uint32_t v[4];
         ss_ld4(acc + uint32_t(c), v);
         if (live) ss_out(a, c, a.M - c, n, scale, sw, b, v);
+        __syncwarp();
       }
       accumulators_read();
     } else {
