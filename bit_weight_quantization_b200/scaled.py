@@ -24,9 +24,11 @@ def _refuse(where: str, what: str):
 
 
 @contextlib.contextmanager
-def _on(device, stream):
+def _on(device, stream, *tensors):
     """`device` current, and `stream` (a torch stream of it) torch's current one: what is allocated inside
-    belongs to the stream that uses it."""
+    belongs to the stream that uses it. `tensors` (None: left out) belong to the streams they were made on, so
+    their memory is marked as used by `stream`: freed by the caller, it is not handed out again before `stream`
+    has come past this call."""
     if stream is not None and not (isinstance(stream, torch.cuda.Stream) and stream.device == device):
         _refuse("stream", "needs a torch.cuda.Stream of the tensors' device")
     with torch.cuda.device(device):
@@ -34,6 +36,9 @@ def _on(device, stream):
             yield
         else:
             with torch.cuda.stream(stream):
+                for t in tensors:
+                    if t is not None:
+                        t.record_stream(stream)
                 yield
 
 
@@ -71,14 +76,15 @@ def empty_codes(rows: int, K: int, device):
 def scaled_quantize(x, gate=None, rows=None, q=None, scale=None, stream=None):
     """Per-row int8 codes and scales of x [*, K] (f32, bf16 or f16; see bq_scaled_quantize in include/bq.h):
     of all rows, or with `rows` (int32 [M]) of row rows[i] for every i (negative: an empty slot); with `gate`
-    of x * SiLU(gate). Returns (q [M, K] int8, scale [M] f32), written to `q` and `scale` where given."""
+    of x * SiLU(gate). Returns (q [M, K] int8, scale [M] f32), written to `q` and `scale` where given.
+    `stream`: as for ScaledLinear."""
     where = "scaled_quantize"
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in _TYPE:
         _refuse(where, "x is a 2-D f32, bf16 or f16 tensor")
     dev, K = x.device, x.shape[1]
     R, ldx = _matrix(x, "x", where, K, dev)
     if _elsewhere(dev, stream):
-        with _on(dev, stream):
+        with _on(dev, stream, x, gate, rows, q, scale):
             return scaled_quantize(x, gate, rows, q, scale)
     ldg, gp, rp, M = 0, None, None, R
     if gate is not None:
@@ -115,7 +121,9 @@ class ScaledLinear:
     are copied once into rows that do. Nothing is kept between calls: outputs and workspaces are
     allocated per call on the stream that runs it (or given, `y`), so calls on several streams and
     several captured graphs do not share memory. `stream` (a torch stream) defaults to torch's
-    current one on the layer's device."""
+    current one on the layer's device. As with torch's own calls the caller orders the streams: what is
+    passed has to be complete on `stream` (Stream.wait_stream), and what is returned belongs to it. Memory
+    passed to a call with `stream` may be freed as soon as the call has returned."""
 
     def __init__(self, codes, scale, bias=None):
         where = "ScaledLinear"
@@ -135,6 +143,7 @@ class ScaledLinear:
         bp = None if bias is None else _vector(bias, "bias", where, E * N, torch.float32, codes.device)
         self.codes, self.scale, self.bias, self.device = c3, scale, bias, codes.device
         self.experts, self.N, self.K = E, N, K
+        self._held = (c3, scale, bias)
         self.weights = bq.bq_scaled_weights(c3.data_ptr(), sp, bp, sn, se, N, K, E)
         self._w = ctypes.byref(self.weights)
         self._workspace = {}  # tokens -> workspace bytes (sizes only; the memory is allocated per call)
@@ -171,7 +180,7 @@ class ScaledLinear:
         if x.dtype not in _TYPE:
             _refuse(where, "x is f32, bf16 or f16")
         if _elsewhere(dev, stream):
-            with _on(dev, stream):
+            with _on(dev, stream, x, y, *self._held):
                 return self.linear(x, y, dtype)
         y, kind, ldy = self._out(y, M, dtype or x.dtype, where)
         n = self._workspace.get(M)
@@ -189,7 +198,7 @@ class ScaledLinear:
         where, dev = "ScaledLinear.gemm", self.device
         M, ldq, sp = self._codes(q, scale, where)
         if _elsewhere(dev, stream):
-            with _on(dev, stream):
+            with _on(dev, stream, q, scale, y, *self._held):
                 return self.gemm(q, scale, y, dtype)
         y, kind, ldy = self._out(y, M, dtype, where)
         st = _gemm(self._w, q.data_ptr(), ldq, sp, M, y.data_ptr(), kind, ldy, _raw_stream(dev.index))
@@ -204,7 +213,7 @@ class ScaledLinear:
         M, ldq, sp = self._codes(q, scale, where)
         op = _vector(offsets, "offsets", where, self.experts + 1, torch.int32, dev)
         if _elsewhere(dev, stream):
-            with _on(dev, stream):
+            with _on(dev, stream, q, scale, offsets, y, *self._held):
                 return self.gemm_grouped(q, scale, offsets, y, dtype)
         y, kind, ldy = self._out(y, M, dtype, where)
         st = _gemm_grouped(self._w, q.data_ptr(), ldq, sp, M, op, y.data_ptr(), kind, ldy, _raw_stream(dev.index))

@@ -77,3 +77,63 @@ def test_one_launch_from_unaligned_rows(M, K, ld, start, name):
     assert np.array_equal(host(q), R.quantize(host(x))[0])
     y_ref, p = R.gemm(host(q), host(s), w, sw)
     check(bq, layer.linear(x, dtype=torch.float32), y_ref, p, "fp32", False)
+
+
+def side_calls(torch, bq):
+    """Every call that takes a stream, as (name, call of fresh inputs on the stream, its inputs)."""
+    g = torch.Generator(device="cuda").manual_seed(21)
+    M, K, N = 200, 1024, 512
+    W = torch.randn(2, N, K, generator=g, device="cuda")
+    one, two = bq.ScaledLinear.quantize(W[0], bias=torch.ones(N, device="cuda")), bq.ScaledLinear.quantize(W)
+    x = torch.randn(M, K, generator=g, device="cuda")
+    q, s = bq.scaled_quantize(x)
+    rows = torch.arange(M - 1, -1, -1, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 77, M], dtype=torch.int32, device="cuda")
+    y = lambda: torch.zeros(M, N, device="cuda")  # noqa: E731
+    held = lambda layer: [layer.codes, layer.scale] + ([] if layer.bias is None else [layer.bias])  # noqa: E731
+    return [
+        ("quantize", lambda st, x, gate, rows, q, s: bq.scaled_quantize(x, gate, rows, q, s, stream=st)[0],
+         lambda: [x.clone(), x.clone(), rows.clone(), torch.zeros_like(q), torch.zeros_like(s)], []),
+        ("linear", lambda st, x, y: one.linear(x, y=y, stream=st), lambda: [x.clone(), y()], held(one)),
+        ("gemm", lambda st, q, s, y: one.gemm(q, s, y=y, stream=st), lambda: [q.clone(), s.clone(), y()], held(one)),
+        ("grouped", lambda st, q, s, off, y: two.gemm_grouped(q, s, off, y=y, stream=st),
+         lambda: [q.clone(), s.clone(), off.clone(), y()], held(two))]
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_memory_passed_to_another_stream_is_recorded_there(which, monkeypatch):
+    torch, bq = mods()
+    name, call, make, held = side_calls(torch, bq)[which]
+    side, seen = torch.cuda.Stream(), []
+    args = make()
+    torch.cuda.synchronize()
+    record = torch.Tensor.record_stream
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, st: (seen.append((t.data_ptr(), st)), record(t, st))[1])
+    call(side, *args)
+    side.synchronize()
+    assert {(t.data_ptr(), side) for t in args + held} <= set(seen), name
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_inputs_freed_behind_a_call_on_another_stream(which):
+    """Inputs that the caller drops while the other stream has not come to the call yet, and new tensors of their
+    sizes that are written at once on the inputs' own stream."""
+    torch, bq = mods()
+    name, call, make, _ = side_calls(torch, bq)[which]
+    side = torch.cuda.Stream()
+    args = make()
+    torch.cuda.synchronize()
+    want = call(side, *args).clone() if name != "quantize" else call(side, *args)
+    side.synchronize()
+    want = want.clone()
+    args = make()
+    sizes = [(a.shape, a.dtype) for a in args[:-1]]  # the last one is an output
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+    got = call(side, *args)
+    del args
+    new = [torch.empty(shape, dtype=dtype, device="cuda").fill_(1) for shape, dtype in sizes for _ in range(2)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(new) == 2 * len(sizes)
+    bq.bq_device_check()
