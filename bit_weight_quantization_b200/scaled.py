@@ -42,6 +42,13 @@ def _on(device, stream, *tensors):
                 yield
 
 
+def _finish(device):
+    """Waits for what the current stream of `device` holds (not in a capture, whose order is the graph's)."""
+    with torch.cuda.device(device):
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+
+
 def _elsewhere(device, stream) -> bool:
     return stream is not None or _current_device() != device.index
 
@@ -118,7 +125,8 @@ class ScaledLinear:
     """A layer (or one per expert) of int8 codes [N, K] (or [E, N, K]) with a scale per output channel.
 
     Holds references to the tensors it is given; `codes` whose rows do not start on 16-byte boundaries
-    are copied once into rows that do. Nothing is kept between calls: outputs and workspaces are
+    are copied once into rows that do. Weights that are made here (that copy, and those of `quantize`) are
+    complete when the layer is: calls on any stream may read them. Nothing is kept between calls: outputs and workspaces are
     allocated per call on the stream that runs it (or given, `y`), so calls on several streams and
     several captured graphs do not share memory. `stream` (a torch stream) defaults to torch's
     current one on the layer's device. As with torch's own calls the caller orders the streams: what is
@@ -137,6 +145,7 @@ class ScaledLinear:
         if (sk != 1 and K > 1) or sn % 16 or sn < K or se % 16 or se < 0 or c3.data_ptr() % 16:
             buf = torch.zeros((E, N, _up(K)), dtype=torch.int8, device=codes.device)
             buf[:, :, :K] = c3
+            _finish(codes.device)
             c3 = buf[:, :, :K]
             sn, se = buf.stride(1), buf.stride(0)
         sp = _vector(scale, "scale", where, E * N, torch.float32, codes.device)
@@ -154,6 +163,7 @@ class ScaledLinear:
         q, s = scaled_quantize(W.reshape(-1, W.shape[-1]))
         ld = _up(W.shape[-1])
         q = q.as_strided(W.shape, (W.shape[-2] * ld, ld, 1)[-W.dim():])
+        _finish(W.device)
         return cls(q, s.view(W.shape[:-1]), bias)
 
     def _out(self, y, M, dtype, where):

@@ -137,3 +137,44 @@ def test_inputs_freed_behind_a_call_on_another_stream(which):
     torch.cuda.synchronize()
     assert torch.equal(got, want) and len(new) == 2 * len(sizes)
     bq.bq_device_check()
+
+
+@pytest.mark.parametrize("made", ["quantize", "laid out"])
+def test_weights_made_by_a_layer_are_complete_for_every_stream(made):
+    """A layer made behind other work on the current stream, and called on a stream that does not wait for it."""
+    torch, bq = mods()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    W = torch.randn(300, 1001, generator=g, device="cuda")
+    x = torch.randn(5, 1001, generator=g, device="cuda")
+    q, s = bq.scaled_quantize(W)
+    tight = q.contiguous()  # rows of 1001 bytes
+    want = bq.ScaledLinear(q, s).linear(x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    layer = bq.ScaledLinear.quantize(W) if made == "quantize" else bq.ScaledLinear(tight, s)
+    assert torch.cuda.current_stream().query()
+    y = layer.linear(x, stream=side)
+    side.synchronize()
+    assert torch.equal(y, want)
+    bq.bq_device_check()
+
+
+def test_a_layer_can_be_made_in_a_captured_graph():
+    torch, bq = mods()
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(3, 77, generator=g, device="cuda")
+    W = torch.randn(40, 77, generator=g, device="cuda")
+    want = bq.ScaledLinear.quantize(W).linear(x)
+    q, s = bq.scaled_quantize(W)
+    tight, y, z = q.contiguous(), torch.zeros(3, 40, device="cuda"), torch.zeros(3, 40, device="cuda")
+
+    def step():
+        bq.ScaledLinear.quantize(W).linear(x, y=y)
+        bq.ScaledLinear(tight, s).linear(x, y=z)
+    graph = bq.StepGraph(step)
+    y.zero_(), z.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(z, want)
+    bq.bq_device_check()
