@@ -19,8 +19,15 @@ _gemm_grouped, _linear = bq._lib.bq_scaled_gemm_grouped, bq._lib.bq_scaled_linea
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
 
 
+_INT32 = 0x7FFFFFFF  # sizes are passed as int32, which ctypes cuts without a word
+
+
 def _refuse(where: str, what: str):
     raise bq.BQError(bq.BQ_ERR_INVALID_ARG, f"{where}: {what}")
+
+
+def _too_large(where: str, what: str):
+    raise bq.BQError(bq.BQ_ERR_SIZE, f"{where}: {what} has more than 2^31 - 1 rows or columns")
 
 
 @contextlib.contextmanager
@@ -61,6 +68,8 @@ def _matrix(t, name, where, columns, device):
     ld, step = t.stride()
     if cols != columns or (step != 1 and cols > 1) or t.device != device:
         _refuse(where, f"{name} has {cols} columns ({columns} wanted), column stride {step}, on {t.device} ({device})")
+    if rows > _INT32 or cols > _INT32:
+        _too_large(where, name)
     return rows, (ld if rows > 1 else max(ld, cols))
 
 
@@ -102,6 +111,8 @@ def scaled_quantize(x, gate=None, rows=None, q=None, scale=None, stream=None):
     if rows is not None:
         M = rows.shape[0] if rows.dim() == 1 else -1
         rp = _vector(rows, "rows", where, M, torch.int32, dev)
+        if M > _INT32:
+            _too_large(where, "rows")
     if q is None:
         q, ldq = x.new_empty_strided((M, K), (_up(K), 1), dtype=torch.int8), _up(K)
     else:
@@ -140,6 +151,8 @@ class ScaledLinear:
             _refuse(where, "codes is a CUDA int8 tensor [N, K] or [E, N, K]")
         c3 = codes if codes.dim() == 3 else codes[None]
         E, N, K = c3.shape
+        if max(E, N, K) > _INT32:
+            _too_large(where, "codes")
         se, sn, sk = c3.stride()
         sn, se = (sn if N > 1 else _up(K)), (se if E > 1 else 0)
         if (sk != 1 and K > 1) or sn % 16 or sn < K or se % 16 or se < 0 or c3.data_ptr() % 16:

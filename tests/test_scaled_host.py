@@ -156,3 +156,41 @@ def test_header_documents_every_scaled_call():
     for n in bq.EXPORTED:
         if n.startswith("bq_scaled"):
             assert re.search(rf"\b{n}\s*\(", code)
+
+
+@pytest.fixture
+def cuda_like():
+    """Tensors that say they are on a GPU and have no memory: what the calls check before they use one."""
+    import torch
+    from torch._subclasses import FakeTensorMode
+
+    def make(*shape, dtype=torch.bfloat16):
+        with FakeTensorMode():
+            return torch.empty(shape, device="cuda", dtype=dtype)
+    return make
+
+
+@pytest.mark.parametrize("shape", [(2 ** 32 + 4, 1), (2 ** 31, 8), (1, 2 ** 32 + 64), (3, 2 ** 31)])
+def test_sizes_past_32_bits_are_refused(shape, cuda_like):
+    """Sizes go to the library as int32: cut to it, 2^32 + 4 rows would be 4."""
+    import torch
+    with pytest.raises(bq.BQError) as e:
+        bq.scaled_quantize(cuda_like(*shape))
+    assert e.value.status == SIZE
+    with pytest.raises(bq.BQError) as e:
+        bq.ScaledLinear(cuda_like(*shape, dtype=torch.int8), cuda_like(shape[0], dtype=torch.float32))
+    assert e.value.status == SIZE
+    with pytest.raises(bq.BQError) as e:
+        bq.ScaledLinear(cuda_like(2 ** 32 + 1, 1, 1, dtype=torch.int8), cuda_like(2 ** 32 + 1, dtype=torch.float32))
+    assert e.value.status == SIZE
+
+
+def test_gathers_past_32_bits_are_refused(cuda_like, monkeypatch):
+    import torch
+    from bit_weight_quantization_b200 import scaled
+    monkeypatch.setattr(scaled, "_elsewhere", lambda device, stream: False)
+    monkeypatch.setattr(scaled, "_vector", lambda *a: 256)
+    monkeypatch.setattr(torch.Tensor, "data_ptr", lambda t: 256)
+    with pytest.raises(bq.BQError) as e:
+        bq.scaled_quantize(cuda_like(4, 16), rows=cuda_like(2 ** 32 + 4, dtype=torch.int32))
+    assert e.value.status == SIZE
