@@ -109,7 +109,9 @@ def scaled_quantize(x, gate=None, rows=None, q=None, scale=None, stream=None):
             _refuse(where, f"gate is {R} rows of {x.dtype}")
         gp = gate.data_ptr()
     if rows is not None:
-        M = rows.shape[0] if rows.dim() == 1 else -1
+        if not isinstance(rows, torch.Tensor) or rows.dim() != 1:
+            _refuse(where, "rows is a 1-D int32 tensor")
+        M = rows.shape[0]
         rp = _vector(rows, "rows", where, M, torch.int32, dev)
         if M > _INT32:
             _too_large(where, "rows")
@@ -173,6 +175,8 @@ class ScaledLinear:
     @classmethod
     def quantize(cls, W, bias=None):
         """Codes and scales of W [N, K] or [E, N, K] (f32, bf16 or f16), one scale per output channel."""
+        if not isinstance(W, torch.Tensor) or W.dim() not in (2, 3):
+            _refuse("ScaledLinear.quantize", "W is a tensor [N, K] or [E, N, K]")
         q, s = scaled_quantize(W.reshape(-1, W.shape[-1]))
         ld = _up(W.shape[-1])
         q = q.as_strided(W.shape, (W.shape[-2] * ld, ld, 1)[-W.dim():])

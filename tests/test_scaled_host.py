@@ -194,3 +194,19 @@ def test_gathers_past_32_bits_are_refused(cuda_like, monkeypatch):
     with pytest.raises(bq.BQError) as e:
         bq.scaled_quantize(cuda_like(4, 16), rows=cuda_like(2 ** 32 + 4, dtype=torch.int32))
     assert e.value.status == SIZE
+
+
+def test_arguments_of_another_kind_are_refused(cuda_like, monkeypatch):
+    import torch
+    from bit_weight_quantization_b200 import scaled
+    monkeypatch.setattr(scaled, "_elsewhere", lambda device, stream: False)
+    monkeypatch.setattr(torch.Tensor, "data_ptr", lambda t: 256)
+    x = cuda_like(4, 16)
+    for call in (lambda: bq.scaled_quantize(x, rows=[0, 1]), lambda: bq.scaled_quantize(x, rows=cuda_like(2, 2, dtype=torch.int32)),
+                 lambda: bq.scaled_quantize(x, rows=cuda_like(dtype=torch.int32)), lambda: bq.scaled_quantize(x, gate=1.0),
+                 lambda: bq.scaled_quantize(None), lambda: bq.ScaledLinear.quantize(cuda_like(16)),
+                 lambda: bq.ScaledLinear.quantize(cuda_like(1, 2, 4, 16)), lambda: bq.ScaledLinear.quantize(None),
+                 lambda: bq.ScaledLinear(cuda_like(4, 16, dtype=torch.int8), 1.0)):
+        with pytest.raises(bq.BQError) as e:
+            call()
+        assert e.value.status == INVALID
