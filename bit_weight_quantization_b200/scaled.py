@@ -33,9 +33,9 @@ def _too_large(where: str, what: str):
 @contextlib.contextmanager
 def _on(device, stream, *tensors):
     """`device` current, and `stream` (a torch stream of it) torch's current one: what is allocated inside
-    belongs to the stream that uses it. `tensors` (None: left out) belong to the streams they were made on, so
-    their memory is marked as used by `stream`: freed by the caller, it is not handed out again before `stream`
-    has come past this call."""
+    belongs to the stream that uses it. `tensors` belong to the streams they were made on, so their memory is
+    marked as used by `stream`: freed by the caller, it is not handed out again before `stream` has come past
+    this call. (What is None or no tensor of `device` is left to the call's own checks.)"""
     if stream is not None and not (isinstance(stream, torch.cuda.Stream) and stream.device == device):
         _refuse("stream", "needs a torch.cuda.Stream of the tensors' device")
     with torch.cuda.device(device):
@@ -44,7 +44,7 @@ def _on(device, stream, *tensors):
         else:
             with torch.cuda.stream(stream):
                 for t in tensors:
-                    if t is not None:
+                    if isinstance(t, torch.Tensor) and t.device == device:
                         t.record_stream(stream)
                 yield
 

@@ -178,3 +178,26 @@ def test_a_layer_can_be_made_in_a_captured_graph():
     torch.cuda.synchronize()
     assert torch.equal(y, want) and torch.equal(z, want)
     bq.bq_device_check()
+
+
+def test_calls_on_another_stream_refuse_what_others_refuse():
+    torch, bq = mods()
+    side = torch.cuda.Stream()
+    layer = bq.ScaledLinear(torch.ones(16, 64, dtype=torch.int8, device="cuda"), torch.ones(16, device="cuda"))
+    x = torch.ones(4, 64, device="cuda")
+    q, s = bq.scaled_quantize(x)
+    off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    bad = [lambda st: bq.scaled_quantize(x, gate=1, stream=st), lambda st: bq.scaled_quantize(x, rows=[0], stream=st),
+           lambda st: bq.scaled_quantize(x, q=q.cpu(), stream=st), lambda st: bq.scaled_quantize(x, scale=s.cpu(), stream=st),
+           lambda st: layer.linear(x, y=torch.empty(4, 16), stream=st), lambda st: layer.linear(x, y=5, stream=st),
+           lambda st: layer.gemm(q, s, y=[], stream=st), lambda st: layer.gemm_grouped(q, s, off.cpu(), stream=st)]
+    for i, call in enumerate(bad):
+        for st in (None, side):
+            with pytest.raises(bq.BQError) as e:
+                call(st)
+            assert e.value.status == bq.BQ_ERR_INVALID_ARG, i
+    for st in (0, torch.cuda.current_stream().cuda_stream, "side"):
+        with pytest.raises(bq.BQError):
+            layer.linear(x, stream=st)
+    torch.cuda.synchronize()
+    bq.bq_device_check()
