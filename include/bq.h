@@ -392,9 +392,9 @@ bq_status bq_scaled_quantize(const void* x, int32_t x_type, int64_t ldx, int32_t
                              float* scale, void* stream);
 
 /* y[m][n] = (float)(sum_k q[m][k] codes[n][k]) * (scale[m] * w.scale[n]) + w.bias[n], one expert.
- * The sum is exact (int32; codes may be -128). The sum, the product of the scales, their product
- * and the sum with the bias are each rounded to f32 (a bias is added by one fused multiply-add),
- * then y is rounded once to y_type. */
+ * The sum is exact (int32; codes may be -128). S = the sum rounded to f32, s = scale[m] * w.scale[n]
+ * rounded to f32. Without a bias S * s is rounded to f32; with one S * s + bias is, once (a fused
+ * multiply-add: the product itself is not rounded). Then y is rounded once to y_type. */
 bq_status bq_scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_t ldq, const float* scale, int32_t M,
                          void* y, int32_t y_type, int64_t ldy, void* stream);
 

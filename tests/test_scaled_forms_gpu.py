@@ -201,3 +201,44 @@ def test_calls_on_another_stream_refuse_what_others_refuse():
             layer.linear(x, stream=st)
     torch.cuda.synchronize()
     bq.bq_device_check()
+
+
+def rounded_sum(p, b):
+    """p + b (f64 arrays) rounded once to f32: the f64 sum is rounded to odd, so that no tie of f32 is made."""
+    s = p + b
+    bb = s - p
+    err = (p - (s - bb)) + (b - bb)  # the exact remainder
+    odd = (s.view(np.int64) & 1).astype(bool)
+    s = np.where((err != 0) & ~odd, np.nextafter(s, np.where(err > 0, np.inf, -np.inf)), s)
+    return s.astype(np.float32)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("M", [1, 7, 40, 100, 300])
+def test_products_take_the_documented_roundings(M, bias):
+    """Bit for bit in f32, and its nearest value in the 16-bit types: fl(fl(sum) * fl(sa sw)), or with a bias
+    fl(fl(sum) * fl(sa sw) + bias) from the unrounded product."""
+    torch, bq = mods()
+    rng = np.random.default_rng(M)
+    N, K = 333, 2000
+    w, wd = codes(torch, rng, N, K)
+    q, qd = codes(torch, rng, M, K)
+    q[0, :], w[0, :] = 127, 127  # a sum past 2^24 among them
+    qd[0], wd[0] = 127, 127
+    sw, swd = scales(torch, rng, N)
+    sa, sad = scales(torch, rng, M)
+    b = rng.standard_normal(N).astype(np.float32) if bias else None
+    acc = (q.astype(np.int64) @ w.astype(np.int64).T).astype(np.float32)
+    s = sa[:, None] * sw[None, :]
+    assert s.dtype == np.float32
+    want = rounded_sum(acc.astype(np.float64) * s.astype(np.float64), np.broadcast_to(b.astype(np.float64), acc.shape)) \
+        if bias else acc * s
+    layer = bq.ScaledLinear(wd, swd, torch.from_numpy(b).cuda() if bias else None)
+    whole = layer.gemm(qd, sad, dtype=torch.float32)
+    off = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    by_expert = layer.gemm_grouped(qd, sad, off, dtype=torch.float32)
+    assert np.array_equal(host(whole), want) and torch.equal(whole, by_expert)
+    for t in (torch.bfloat16, torch.float16):
+        assert torch.equal(layer.gemm(qd, sad, dtype=t), whole.to(t))
+        assert torch.equal(layer.gemm_grouped(qd, sad, off, dtype=t), whole.to(t))
+    bq.bq_device_check()
