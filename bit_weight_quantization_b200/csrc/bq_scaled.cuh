@@ -248,8 +248,12 @@ __global__ void __launch_bounds__(1024) k_scaled_quantize_long(const SqArgs a) {
 // Large products are bound by the tensor cores and, over milliseconds, by the board's power:
 // 8192 x 13824 x 5120 in 359 us (3.23 POPS; tensor pipe 93 % active), 424 us in a loop of seconds.
 //
-// Every wait is bounded and ends when another role has stopped; then the error word is raised,
-// the peer is told, copies in flight are waited for and the tensor memory is freed.
+// Every wait on an mbarrier is bounded and ends when another role has stopped; then the error word is
+// raised, the peer is told, copies in flight are waited for and the tensor memory is freed. Three waits have
+// no bound: for the kernel before (it ends by itself), for tensor memory (whatever holds some comes to its
+// end: a pair shares its SMs with nothing that leaves it too few columns, see plan_scaled_gemm, and the split
+// kernel waits for no peer while it holds some), and at the cluster's barrier (its CTAs start together, and each
+// arrives on every path).
 
 constexpr int kSgThreads = 192;
 constexpr int kSgCopyWarp = 4, kSgMmaWarp = 5;

@@ -398,8 +398,10 @@ bq_status bq_scaled_quantize(const void* x, int32_t x_type, int64_t ldx, int32_t
 bq_status bq_scaled_gemm(const bq_scaled_weights* w, const int8_t* q, int64_t ldq, const float* scale, int32_t M,
                          void* y, int32_t y_type, int64_t ldy, void* stream);
 
-/* Launches: every scaled call is launched with programmatic dependent launch, waits for the work
- * before it before it touches memory, and lets the next kernel start only after that. */
+/* Launches: every kernel of the scaled calls is launched with programmatic dependent launch, waits for
+ * the work before it before it touches memory, and lets the next kernel start only after that. One reads
+ * earlier: behind the quantization of the same bq_scaled_linear, which has waited, the product's
+ * kernel fetches weights while the quantization runs. */
 
 /* bq_scaled_gemm with expert e's weights for the rows offsets[e] <= m < offsets[e+1]; `offsets`
  * (device int32 [experts + 1]) is read by the kernel, so no host synchronization is needed and a
