@@ -242,3 +242,280 @@ def test_products_take_the_documented_roundings(M, bias):
         assert torch.equal(layer.gemm(qd, sad, dtype=t), whole.to(t))
         assert torch.equal(layer.gemm_grouped(qd, sad, off, dtype=t), whole.to(t))
     bq.bq_device_check()
+
+
+def test_c_calls_by_their_own_names():
+    """The C calls of the binding, on pointers and sizes, give what the torch layer gives."""
+    torch, bq = mods()
+    g = torch.Generator(device="cuda").manual_seed(31)
+    M, N, K = 9, 50, 100
+    W = torch.randn(2, N, K, generator=g, device="cuda")
+    two, one = bq.ScaledLinear.quantize(W), bq.ScaledLinear.quantize(W[0])
+    x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    q, s = bq.scaled_quantize(x)
+    q2, s2 = bq.empty_codes(M, K, x.device), torch.zeros(M, device="cuda")
+    assert q2.stride(0) == 112
+    bq.bq_scaled_quantize(x, bq.BQ_TYPE_BF16, K, M, None, 0, None, M, K, q2, 112, s2)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+    assert torch.equal(bq.scaled_quantize(x, q=bq.empty_codes(M, K, x.device))[0], q)
+    y = torch.zeros(M, N, device="cuda")
+    bq.bq_scaled_gemm(one.weights, q, 112, s, M, y, bq.BQ_TYPE_F32, N)
+    assert torch.equal(y, one.gemm(q, s, dtype=torch.float32))
+    off = torch.tensor([0, 4, M], dtype=torch.int32, device="cuda")
+    bq.bq_scaled_gemm_grouped(two.weights, q, 112, s, M, off, y, bq.BQ_TYPE_F32, N)
+    assert torch.equal(y, two.gemm_grouped(q, s, off, dtype=torch.float32))
+    n = bq.bq_scaled_workspace_bytes(one.weights, M)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    bq.bq_scaled_linear(one.weights, x, bq.BQ_TYPE_BF16, K, M, y, bq.BQ_TYPE_F32, N, ws, n)
+    assert torch.equal(y, one.linear(x, dtype=torch.float32))
+    with pytest.raises(bq.BQError):
+        bq.bq_scaled_linear(one.weights, x, bq.BQ_TYPE_BF16, K, M, y, bq.BQ_TYPE_F32, N, ws, n - 1)
+    bq.bq_device_check()
+
+
+# ---------------------------------------------------------------------------------------------------
+# quantization of many rows
+# ---------------------------------------------------------------------------------------------------
+
+# rows x K, each more than 148 * 1024 runs of eight elements: the kernels with several runs a thread, for K up to
+# 1024, up to 16384, up to 32768 and above
+MANY = [(1300, 1000), (2400, 513), (1185, 1024), (1180, 1025), (300, 4096), (297, 4099), (120, 11008), (150, 16384), (64, 20001),
+        (40, 32768), (20, 40000), (5, 65536)]
+
+
+def special(torch, x):
+    """Rows of every kind among ordinary ones, in x."""
+    K = x.shape[1]
+    x[1] = 0
+    x[2, K // 3] = float("nan")
+    x[3, K - 1] = float("inf")
+    x[-1, 0] = float("-inf")
+    x[4] *= 2.0 ** -20
+    if x.dtype != torch.float16:
+        x[0] *= 2.0 ** -110
+        x[-2] *= 2.0 ** 100
+    return x
+
+
+def rows_of(torch, M, K, name, seed, ld=None):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    ld = ld or K
+    return (torch.randn(M, ld, generator=g, device="cuda") * 3).to(kind(torch, name))[:, :K]
+
+
+def same_codes(torch, bq, q, s, v, rows=None):
+    bq.bq_device_check()
+    qr, sr = R.quantize(v, rows)
+    assert np.array_equal(host(q), qr)
+    sg = host(s).astype(np.float64)
+    assert np.array_equal(np.isnan(sg), np.isnan(sr))
+    ok = ~np.isnan(sr)
+    assert np.all(np.abs(sg[ok] - sr[ok]) <= R.U * sr[ok])
+
+
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("name", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,K", MANY)
+def test_quantize_many_rows(M, K, name, odd):
+    torch, bq = mods()
+    x = special(torch, rows_of(torch, M, K, name, M + K, K + 3 if odd else (K + 7) // 8 * 8))
+    q, s = bq.scaled_quantize(x)
+    same_codes(torch, bq, q, s, host(x))
+
+
+@pytest.mark.parametrize("name", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,K", MANY[::2] + [(9, 100)])
+def test_quantize_many_gathered_rows(M, K, name):
+    torch, bq = mods()
+    x = special(torch, rows_of(torch, max(M // 3, 8), K, name, M + K))
+    rng = np.random.default_rng(M)
+    rows = rng.integers(-1, x.shape[0], M).astype(np.int32)  # repeated ones and empty slots
+    q, s = bq.scaled_quantize(x, rows=torch.from_numpy(rows).cuda())
+    same_codes(torch, bq, q, s, host(x), rows)
+
+
+def check_gated(bq, q, s, up, gate, rows=None):
+    """The bounds of the gated codes: v = x (g / (1 + exp(-g))) in f32 is within 7 half steps (four for 1 + exp(-g),
+    one each for the sum, the quotient and the product), a code carries v's and gamma's and three more."""
+    bq.bq_device_check()
+    v = R.gated(up, gate)
+    if rows is not None:
+        v = np.where((rows >= 0)[:, None], v[np.maximum(rows, 0)], 0)
+    bad = ~np.isfinite(v).all(1)
+    q, s = host(q).astype(np.float64), host(s).astype(np.float64)
+    assert np.array_equal(np.isnan(s), bad) and np.all(q[bad] == 0)
+    v, q, s = v[~bad], q[~bad], s[~bad]
+    gamma, rel = np.abs(v).max(1), 7 * R.U
+    assert np.all(np.abs(s - gamma / 127) <= 1.01 * (rel + R.U) * gamma / 127)
+    live = gamma > 0
+    assert np.all(q[~live] == 0)
+    exact = v[live] * (127 / gamma[live])[:, None]
+    assert np.all(np.abs(q[live] - exact) <= 0.5 + 1.01 * 127 * (2 * rel + 3 * R.U))
+
+
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("name", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,K", MANY + [(5, 33)])
+def test_quantize_many_gated_rows(M, K, name, odd):
+    """Gate and up side by side in one matrix, whole and (rows with gate) gathered."""
+    torch, bq = mods()
+    both = rows_of(torch, M, 2 * K + (1 if odd else 0), name, M * 3 + K)
+    gate, up = both[:, :K], both[:, K:2 * K]
+    up[1] = 0
+    up[2, K // 2] = float("nan")
+    gate[3, K - 1] = float("inf")
+    gate[-1, 0] = float("-inf")  # -inf / (1 + inf) is no number
+    q, s = bq.scaled_quantize(up, gate=gate)
+    check_gated(bq, q, s, host(up), host(gate))
+    rng = np.random.default_rng(K)
+    rows = rng.integers(-1, M, M).astype(np.int32)
+    q, s = bq.scaled_quantize(up, gate=gate, rows=torch.from_numpy(rows).cuda())
+    check_gated(bq, q, s, host(up), host(gate), rows)
+
+
+# ---------------------------------------------------------------------------------------------------
+# special rows in one launch
+# ---------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("name", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,K", [(1, 200), (2, 200), (1, 4096), (2, 4099), (1, 16384), (2, 16384), (2, 16385)])
+def test_special_rows_in_one_launch(M, K, name):
+    torch, bq = mods()
+    rng = np.random.default_rng(K)
+    w, wd = codes(torch, rng, 300, K)
+    sw, swd = scales(torch, rng, 300)
+    b = rng.standard_normal(300).astype(np.float32)
+    layer = bq.ScaledLinear(wd, swd, torch.from_numpy(b).cuda())
+    base = rows_of(torch, M, K, name, K)
+
+    def put(v, at):
+        return lambda x: x[-1].__setitem__(at, v)
+    kinds = [lambda x: x[-1].zero_(), lambda x: x[-1].fill_(-0.0), put(float("nan"), K // 2), put(float("inf"), 0),
+             put(float("-inf"), K - 1), lambda x: x[-1].zero_()[K - 1:].fill_(2.0 ** -24), lambda x: x[-1].mul_(2.0 ** -15)]
+    if name != "fp16":
+        kinds += [lambda x: x[-1].mul_(2.0 ** -110), lambda x: x[-1].zero_()[3:4].fill_(2.0 ** -100),
+                  lambda x: x[-1].zero_()[3:4].fill_(2.0 ** -101), lambda x: x[-1].mul_(2.0 ** 120)]
+    for i, change in enumerate(kinds):
+        x = base.clone()
+        change(x)
+        y = layer.linear(x, dtype=torch.float32)
+        q, s = bq.scaled_quantize(x)
+        same_codes(torch, bq, q, s, host(x))
+        two = layer.gemm(q, s, dtype=torch.float32)
+        assert torch.equal(torch.nan_to_num(y, nan=1e9), torch.nan_to_num(two, nan=1e9)), i
+        if torch.isnan(s[-1]):
+            assert torch.isnan(y[-1]).all() and not torch.isnan(y[:-1]).any(), i
+        elif s[-1] == 0:
+            assert np.array_equal(host(y[-1]), b), i
+    bq.bq_device_check()
+
+
+# ---------------------------------------------------------------------------------------------------
+# several tiles a CTA
+# ---------------------------------------------------------------------------------------------------
+
+# whole products of three tiles a pair and more, every width of a tile among them (tests/test_scaled_plan.py
+# holds the list to that): M, N, K
+TILES = [(4100, 4104, 640), (3000, 5000, 1111), (2048, 8200, 1800), (493, 7801, 130), (630, 14140, 1800), (5504, 2124, 2100),
+         (1100, 9001, 130), (300, 30000, 400), (9000, 2056, 520)]
+
+
+def near(torch, bq, y, q, sa, w, sw, b, name):
+    """Every output against the exact sums in 64 bits, on the device, with the tolerance of tests/scaled_ref.py."""
+    bq.bq_device_check()
+    p = q.double() @ w.double().t() * sa.double()[:, None] * sw.double()
+    ref = p if b is None else p + b.double()
+    p, size = p.abs(), ref.abs()
+    first = 2 * R.U * p + R.U * size if b is not None else 3 * R.U * p
+    off = (y.double() - ref).abs() / (1.01 * (first + R.HALF_STEP[name] * (size + first)) + R.SMALLEST[name])
+    assert float(off.max()) <= 1, (float(off.max()), (off > 1).nonzero()[:4].tolist())
+
+
+def device_case(torch, M, N, K, seed, bias, lead=()):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def matrix(*shape):
+        ld = (K + 15) // 16 * 16
+        return torch.randint(-128, 128, (*shape, ld), generator=g, device="cuda", dtype=torch.int8)[..., :K]
+    r = lambda *shape: torch.rand(*shape, generator=g, device="cuda") * 2e-3 + 1e-4  # noqa: E731
+    return (matrix(*lead, N), r(*lead, N), torch.randn(*lead, N, generator=g, device="cuda") if bias else None, matrix(M), r(M))
+
+
+@pytest.mark.parametrize("name", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,N,K", TILES)
+def test_several_tiles_a_pair(M, N, K, name):
+    torch, bq = mods()
+    w, sw, b, q, sa = device_case(torch, M, N, K, M + N + K, (M + K) % 200 < 100)
+    layer = bq.ScaledLinear(w, sw, b)
+    near(torch, bq, layer.gemm(q, sa, dtype=kind(torch, name)), q, sa, w, sw, b, name)
+    # rows of y that TMA does not take
+    wide = torch.full((M, N + 1), 7.0, dtype=kind(torch, name), device="cuda")
+    near(torch, bq, layer.gemm(q, sa, y=wide[:, :N]), q, sa, w, sw, b, name)
+    assert torch.all(wide[:, N] == 7)
+
+
+@pytest.mark.parametrize("M,N,K", TILES[:3])
+def test_linear_of_several_tiles_a_pair(M, N, K):
+    """The product behind its own quantization, whose weights are fetched ahead for a pair's first tile only."""
+    torch, bq = mods()
+    w, sw, b, _, _ = device_case(torch, M, N, K, M + N, True)
+    x = rows_of(torch, M, K, "bf16", M)
+    layer = bq.ScaledLinear(w, sw, b)
+    q, s = bq.scaled_quantize(x)
+    qr, _ = R.quantize(host(x))
+    assert np.array_equal(host(q), qr)
+    for _ in range(3):
+        y = layer.linear(x)
+        near(torch, bq, y, q, s, w, sw, b, "bf16")
+
+
+# experts, rows an expert at most, N, K: single CTAs and pairs, three tiles each and more; few hot experts
+GROUPED = [(64, 40, 5000, 1800, "even"), (64, 60, 4100, 130, "even"), (40, 30, 9000, 640, "even"), (8, 800, 3000, 1700, "even"),
+           (16, 400, 4104, 640, "even"), (64, 100, 2048, 520, "one"), (128, 30, 2060, 700, "one"), (48, 200, 9000, 1000, "few")]
+
+
+def counts_of(E, most, N, how):
+    rng = np.random.default_rng(E + N)
+    counts = rng.integers(0, most + 1, E)
+    if how == "one":  # half of the rows are one expert's
+        counts[E // 3] += counts.sum()
+    if how == "few":
+        counts[rng.random(E) < 0.8] = 0
+    return counts
+
+
+@pytest.mark.parametrize("name", ["bf16", "fp32"])
+@pytest.mark.parametrize("E,most,N,K,how", GROUPED)
+def test_grouped_of_several_tiles_a_cta(E, most, N, K, how, name):
+    torch, bq = mods()
+    counts = counts_of(E, most, N, how)
+    before, after = 3, 5
+    M = before + int(counts.sum()) + after
+    w, sw, b, q, sa = device_case(torch, M, N, K, E * N, name == "fp32", (E,))
+    edges = before + np.concatenate([[0], np.cumsum(counts)])
+    y = torch.full((M, N), 7.0, dtype=kind(torch, name), device="cuda")
+    bq.ScaledLinear(w, sw, b).gemm_grouped(q, sa, torch.from_numpy(edges.astype(np.int32)).cuda(), y=y)
+    for e in range(E):
+        r = slice(int(edges[e]), int(edges[e + 1]))
+        if counts[e]:
+            near(torch, bq, y[r], q[r], sa[r], w[e], sw[e], None if b is None else b[e], name)
+    assert torch.all(y[:before] == 7) and torch.all(y[M - after:] == 7)
+
+
+def test_experts_of_any_stride():
+    """Experts interleaved row by row ([N, E, K]), and ones with a gap that is no whole row: views, not copied."""
+    torch, bq = mods()
+    E, N, K = 5, 200, 320
+    g = torch.Generator(device="cuda").manual_seed(6)
+    flat = torch.randint(-128, 128, (E * (N * K + 48),), generator=g, device="cuda", dtype=torch.int8)
+    sw, q, sa = (torch.rand(E, N, generator=g, device="cuda"), flat[:300 * K].view(300, K).flip(1).contiguous(),
+                 torch.rand(300, generator=g, device="cuda"))
+    off = torch.tensor([0, 10, 10, 150, 151, 300], dtype=torch.int32, device="cuda")
+    for w in (flat[:E * N * K].view(N, E, K).transpose(0, 1), flat.as_strided((E, N, K), (N * K + 48, K, 1))):
+        layer = bq.ScaledLinear(w, sw)
+        assert layer.codes.data_ptr() == flat.data_ptr()
+        y = layer.gemm_grouped(q, sa, off, dtype=torch.float32)
+        for e in range(E):
+            r = slice(int(off[e]), int(off[e + 1]))
+            if r.stop > r.start:
+                near(torch, bq, y[r], q[r], sa[r], w[e], sw[e], None, "fp32")

@@ -109,3 +109,23 @@ def test_no_allocation_of_tensor_memory_has_to_wait_beside_a_pair(plans):
     for bn, cols, smem in pairs:
         left = 228 * KB - (smem + KB)
         assert cols + density * left <= COLS, (bn, cols, smem)
+
+
+def test_gpu_cases_take_a_third_tile(plans):
+    """The whole-output comparisons of tests/test_scaled_forms_gpu.py: every width of a pair's tile, single CTAs
+    and pairs, and more than two tiles each (an accumulator is used again from the third on)."""
+    from tests.test_scaled_forms_gpu import GROUPED, TILES, counts_of
+    widths, deep = set(), 0
+    for (_, M, N, K, *_), (cg, bn, stages, *_) in plans([("tc", M, N, K, 1, 0, 1) for M, N, K in TILES]):
+        assert cg == 2 and -(-M // bn) * -(-N // 256) > 2 * 74, (M, N, K)
+        widths.add(bn)
+        deep += -(-K // 128) > stages
+    assert widths == set(range(64, 257, 32)) and deep >= 3
+    kinds = []
+    for E, most, N, K, how in GROUPED:
+        counts = counts_of(E, most, N, how)
+        [(_, (cg, bn, stages, *_))] = plans([("tc", int(counts.sum()) + 8, N, K, E, 1, 1)])
+        tiles = sum(-(-int(c) // bn) for c in counts) * -(-N // (128 * cg))
+        assert tiles > 2 * (74 if cg == 2 else 296), (E, N)
+        kinds.append((cg, -(-K // 128) > stages))
+    assert set(kinds) == {(1, True), (1, False), (2, True), (2, False)}
