@@ -57,7 +57,7 @@ template <typename T, bool GATE>
 inline cudaError_t launch_scaled_quantize(const SqArgs& a, cudaStream_t s) {
   const int runs = (a.K + 7) / 8;
   if (runs > 4096) return launch_pdl(k_scaled_quantize_long<T, GATE>, dim3(unsigned(a.M)), dim3(1024), 0, s, a);
-  if ((long long)a.M * runs <= 148 * 1024 || runs <= 64) {
+  if ((long long)a.M * runs <= sm_count() * 1024 || runs <= 64) {
     if (runs <= 1024) return launch_scaled_rows<T, GATE, 1, 1024, 1>(a, s);
     if (runs <= 2048) return launch_scaled_rows<T, GATE, 2, 1024, 1>(a, s);
     return launch_scaled_rows<T, GATE, 4, 1024, 1>(a, s);

@@ -36,17 +36,17 @@ struct SgPlan {
   uint32_t smem;
 };
 
-// Tokens per tile of CTA pairs, for rows of one product (or one expert) on N channels: the choice that
+// Tokens per tile of CTA pairs, for rows of one whole product on N channels: the choice that
 // takes the fewest cycles by this model. A chunk of 128 k costs a pair its four MMAs (138 cycles each at 256
 // tokens, 69 at 128, 47 at 64) or the copies of its operands at 64 bytes a cycle and SM; a wave is as many
 // tiles as there are pairs; the last tile's epilogue, 23 cycles a token, is not hidden. (Measured, 333 x
 // 5120 x 5104: 21.9 us with 256, 17.9 with 128; 256 x 4096 x 4096: 16.8 and, with 64, 11.4.)
-inline int scaled_pair_tokens(long long rows, int groups, int N, int K, int sms) {
+inline int scaled_pair_tokens(long long rows, int N, int K, int sms) {
   const long long nt = (N + 2 * kSgRows - 1) / (2 * kSgRows), kc = (K + kSgChunk - 1) / kSgChunk, pairs = sms / 2;
   int best = 256;
   double best_cost = -1;
   for (int bn = 256; bn >= 64; bn -= 32) {
-    const long long tiles = (rows + bn - 1) / bn * groups * nt, waves = (tiles + pairs - 1) / pairs;
+    const long long tiles = (rows + bn - 1) / bn * nt, waves = (tiles + pairs - 1) / pairs;
     const double chunk = std::max(4.0 * std::max(47.0, 0.54 * bn), (double(kSgWBytes) + 64.0 * bn) / 64.0);
     const double cost = double(waves) * double(kc) * chunk + 23.0 * double(std::min<long long>(bn, rows));
     if (best_cost < 0 || cost < best_cost) { best = bn; best_cost = cost; }
@@ -66,7 +66,7 @@ inline SgPlan plan_scaled_gemm(int M, int N, int K, int E, bool grouped, bool y_
     p.bn = int(std::min<long long>(64, (most + 15) / 16 * 16));
   } else {
     p.cg = 2;
-    p.bn = int(std::min<long long>(grouped ? 256 : scaled_pair_tokens(rows, 1, N, K, sms), (most + 31) / 32 * 32));
+    p.bn = int(std::min<long long>(grouped ? 256 : scaled_pair_tokens(rows, N, K, sms), (most + 31) / 32 * 32));
   }
   p.stage_bytes = int(kSgWBytes) + p.bn / p.cg * kSgChunk;
   p.acc_stride = (p.bn + 31) / 32 * 32;

@@ -158,11 +158,9 @@ class ScaledLinear:
         se, sn, sk = c3.stride()
         sn, se = (sn if N > 1 else _up(K)), (se if E > 1 else 0)
         if (sk != 1 and K > 1) or sn % 16 or sn < K or se % 16 or se < 0 or c3.data_ptr() % 16:
-            buf = torch.zeros((E, N, _up(K)), dtype=torch.int8, device=codes.device)
-            buf[:, :, :K] = c3
+            sn, se = _up(K), N * _up(K)
+            c3 = empty_codes(E * N, K, codes.device).as_strided((E, N, K), (se, sn, 1)).copy_(c3)
             _finish(codes.device)
-            c3 = buf[:, :, :K]
-            sn, se = buf.stride(1), buf.stride(0)
         sp = _vector(scale, "scale", where, E * N, torch.float32, codes.device)
         bp = None if bias is None else _vector(bias, "bias", where, E * N, torch.float32, codes.device)
         self.codes, self.scale, self.bias, self.device = c3, scale, bias, codes.device
