@@ -159,7 +159,8 @@ __device__ __forceinline__ void sq_finish(const SqArgs& a, int i, const SqScale&
 // read once and the gate computed once; blockDim.y rows a block. Bound by memory for f32 and, with 8 runs
 // a thread to spread the fixed cost of a thread over, nearly so for 16-bit types; with the gate by the
 // instruction issue of its exp and divide, for which the registers are held to 40 so that 48 warps fit
-// an SM (60 registers, 22 warps: 95 us for 4096 x 11008 bf16, against 65).
+// an SM (60 registers, 22 warps: 95 us for 4096 x 11008 bf16, against 65.6). That costs spills, 12 words a
+// thread in 16-bit types and 30 in f32 (75.0 us for 4096 x 11008, 5.4 TB/s).
 template <typename T, bool GATE, int C, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) k_scaled_quantize(const SqArgs a) {
   __shared__ uint32_t most[32];

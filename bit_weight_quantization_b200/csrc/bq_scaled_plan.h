@@ -54,6 +54,15 @@ inline int scaled_pair_tokens(long long rows, int N, int K, int sms) {
   return best;
 }
 
+// By expert: single CTAs, two an SM, for 64 rows an expert and fewer on average, pairs above. (Measured with
+// both forced, even rows, pairs / single, in us. 64 experts of 2048 x 2048, f32: 46.5 / 46.2 at 1 row, 49.5 /
+// 48.7 at 16, 51.2 / 50.8 at 32, 52.5 / 53.2 at 48, 54.4 / 54.5 at 64, 54.8 / 58.6 at 72, 57.0 / 62.2 at 96. 16
+// experts of 4096 x 4096, bf16: 47.8 / 43.9, 48.4 / 45.8, 49.2 / 46.3, 51.2 / 48.0, 51.0 / 47.4, 54.0 / 59.6,
+// 54.1 / 60.9. 64 experts of 4096 x 1024, bf16: 56.0 / 45.6, 59.9 / 46.5, 56.8 / 47.2, 64.0 / 49.3, 60.8 / 50.0,
+// 72.5 / 61.8, 71.2 / 65.0: there single CTAs would still win above 64. Rows that differ by up to half either
+// way cost single CTAs more where some pass 64: 16 experts of 56 and 64 rows, 51.5 / 55.4 and 53.3 / 53.6.) Tokens
+// a tile go up to twice the average: a hotter expert takes several tiles and reads its weights again for each.
+//
 // A pair that takes every column of its SMs takes their whole shared memory too, so that no other CTA with
 // tensor memory can lie on either. One could otherwise hold columns on the first SM while it waits for a CTA of
 // its own cluster that waits for columns on the second, which the pair holds while it waits for the first.
