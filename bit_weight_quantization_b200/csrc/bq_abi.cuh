@@ -134,7 +134,9 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e != cudaSuccess) (void)cudaGetLastError();  // launch_status of a later call must not find it
+  return e;
 }
 
 // bq_linear runs an ABQ layer of more than one token as activation quantization into its

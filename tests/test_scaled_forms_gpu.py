@@ -519,3 +519,26 @@ def test_experts_of_any_stride():
             r = slice(int(off[e]), int(off[e + 1]))
             if r.stop > r.start:
                 near(torch, bq, y[r], q[r], sa[r], w[e], sw[e], None, "fp32")
+
+
+def test_a_refused_launch_leaves_no_error_to_the_next_call():
+    """A launch on the legacy stream is refused while a blocking stream is being captured. The call says so, and
+    the next one, which looks for errors of its own launches, finds none."""
+    import ctypes
+    torch, bq = mods()
+    rt = ctypes.CDLL("libcudart.so.12")  # torch's
+    x = torch.randn(4, 64, device="cuda")
+    W = torch.randn(32, 256, device="cuda")
+    q, s = bq.scaled_quantize(x)
+    torch.cuda.synchronize()
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert rt.cudaStreamCreate(ctypes.byref(stream)) == 0
+    assert rt.cudaStreamBeginCapture(stream, 0) == 0
+    status = bq.raw_status("bq_scaled_quantize", x.data_ptr(), bq.BQ_TYPE_F32, 64, 4, None, 0, None, 4, 64, q.data_ptr(),
+                           q.stride(0), s.data_ptr(), None)
+    assert rt.cudaStreamEndCapture(stream, ctypes.byref(graph)) != 0  # the refused launch has ended the capture
+    rt.cudaGetLastError()
+    assert rt.cudaStreamDestroy(stream) == 0
+    assert status == bq.BQ_ERR_CUDA
+    bq.QuantLinear("bitnet", W)
+    bq.bq_device_check()
