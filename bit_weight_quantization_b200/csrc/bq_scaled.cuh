@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(kSgThreads, 1) k_scaled_tc(const __grid_consta
 // s32 sums in the shared memory of the CTA that finishes those tokens (integer sums: exact in any
 // order). The tensor cores keep up with the memory although an MMA of 128 channels costs the same
 // 27 ns for 16 tokens as for 64 (4 KB of weights: 150 GB/s an SM, 22 TB/s in all). Bound by the memory and
-// by the time until its first bytes: 1 x 4096 x 4096 from bf16 in 6.7 us (2.5 TB/s), 1 x 13824 x 5120 in
+// by the time until its first bytes: 1 x 4096 x 4096 from bf16 in 6.6 us (2.5 TB/s), 1 x 13824 x 5120 in
 // 14.7 (4.8 TB/s); from codes 16 x 4096 x 4096 in 6.1, 1 x 13824 x 5120 in 13.8 (5.1 TB/s).
 //
 // T = int8_t: the tokens' codes come by TMA beside the weights. Otherwise x is quantized here, by

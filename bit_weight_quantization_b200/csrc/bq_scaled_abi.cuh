@@ -222,8 +222,9 @@ inline bq_status launch_scaled_fused(const SsArgs& a, cudaStream_t s) {
 }
 
 // Whether bq_scaled_linear quantizes inside the product: up to kSsFusedTokens tokens, as every CTA reads them
-// all (4096 x 4096: one token 6.7 us, two 7.3, four 8.8, in two launches 7.6; 13824 x 5120: one token 14.7, two
-// 16.0, four 23.2, in two launches 15.5), and K <= 16384 so that the operand of any split leaves room for stages.
+// all (4096 x 4096: one token 6.6 us, two 7.5, four 8.8, in two launches 7.6; 13824 x 5120: one token 14.6, two
+// 16.0, four 23.2, in two launches 15.6; at 4096 x 11008 the rule loses: 12.5 and 14.5, four in two launches
+// 12.1), and K <= 16384 so that the operand of any split leaves room for stages.
 inline bool scaled_fused(int M, int K) { return M <= kSsFusedTokens && K <= 16384; }
 
 inline bool split_args(const bq_scaled_weights* w, int M, void* y, int y_type, int64_t ldy, SsArgs* a) {
