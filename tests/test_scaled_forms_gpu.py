@@ -542,3 +542,35 @@ def test_a_refused_launch_leaves_no_error_to_the_next_call():
     assert status == bq.BQ_ERR_CUDA
     bq.QuantLinear("bitnet", W)
     bq.bq_device_check()
+
+
+def test_calls_on_a_forked_stream_of_a_captured_graph():
+    """stream= inside a capture: work forked onto another stream and joined, inputs that do not outlive the step,
+    replayed beside eager calls of the same layers on another stream."""
+    torch, bq = mods()
+    g = torch.Generator(device="cuda").manual_seed(12)
+    layer = bq.ScaledLinear.quantize(torch.randn(300, 1000, generator=g, device="cuda"))
+    xs = [torch.randn(M, 1000, generator=g, device="cuda") for M in (1, 40, 200)]
+    want = [layer.linear(x) for x in xs]
+    ys, side = [torch.zeros_like(y) for y in want], torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        tmp = [x + 0 for x in xs]
+        side.wait_stream(here)
+        for x, y in zip(tmp, ys):
+            layer.linear(x, y=y, stream=side)
+        del tmp, x
+        junk = [torch.full_like(x, 3.0) for x in xs]
+        here.wait_stream(side)
+        return junk
+    graph = bq.StepGraph(step)
+    for _ in range(3):
+        for y in ys:
+            y.zero_()
+        graph.replay()
+        eager = [layer.linear(x, stream=side) for x in xs]
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, w) for y, w in zip(ys, want))
+        assert all(torch.equal(y, w) for y, w in zip(eager, want))
+    bq.bq_device_check()

@@ -96,19 +96,20 @@ def test_no_allocation_of_tensor_memory_has_to_wait_beside_a_pair(plans):
     """The CTAs that share an SM never ask for more columns than it has. A pair that waits for columns on one SM
     while it holds those of the other could be waited for by what holds them."""
     rng = random.Random(2)
-    density, pairs = 0.0, []  # columns per byte of shared memory, of the CTAs that may lie beside others
+    # columns per byte of shared memory, and the least shared memory, of the CTAs that may lie beside others
+    density, least, pairs = 0.0, SMEM, []
     for _, (cg, bn, _, _, cols, _, smem) in plans(whole(rng, 2000) + grouped(rng, 4000)):
         if cg == 2:
             pairs.append((bn, cols, smem))
         else:
-            density = max(density, cols / (smem + KB))
+            density, least = max(density, cols / (smem + KB)), min(least, smem + KB)
     for _, (nn, cols, _, _, _, _, smem) in plans(split(rng, 4000)):
-        density = max(density, cols / (smem + KB))
+        density, least = max(density, cols / (smem + KB)), min(least, smem + KB)
     assert density * 228 * KB <= COLS
     assert any(cols == COLS for _, cols, _ in pairs)
     for bn, cols, smem in pairs:
         left = 228 * KB - (smem + KB)
-        assert cols + density * left <= COLS, (bn, cols, smem)
+        assert left < least or cols + density * left <= COLS, (bn, cols, smem)
 
 
 def test_gpu_cases_take_a_third_tile(plans):
