@@ -139,12 +139,14 @@ class ScaledLinear:
 
     Holds references to the tensors it is given; `codes` whose rows do not start on 16-byte boundaries
     are copied once into rows that do. Weights that are made here (that copy, and those of `quantize`) are
-    complete when the layer is: calls on any stream may read them. Nothing is kept between calls: outputs and workspaces are
-    allocated per call on the stream that runs it (or given, `y`), so calls on several streams and
-    several captured graphs do not share memory. `stream` (a torch stream) defaults to torch's
-    current one on the layer's device. As with torch's own calls the caller orders the streams: what is
-    passed has to be complete on `stream` (Stream.wait_stream), and what is returned belongs to it. Memory
-    passed to a call with `stream` may be freed as soon as the call has returned."""
+    complete when the layer is: calls on any stream may read them.
+
+    Nothing is kept between calls: outputs and workspaces are allocated per call on the stream that runs
+    it (or given, `y`), so calls on several streams and several captured graphs do not share memory.
+    `stream` (a torch stream) defaults to torch's current one on the layer's device. As with torch's own
+    calls the caller orders the streams: what is passed has to be complete on `stream`
+    (Stream.wait_stream), and what is returned belongs to it. Memory passed to a call with `stream` may be
+    freed as soon as the call has returned."""
 
     def __init__(self, codes, scale, bias=None):
         where = "ScaledLinear"
